@@ -22,6 +22,8 @@ DEVERR_BAD_ID, DEVERR_NAN_LOGIT, DEVERR_NAN_SCALE, DEVERR_TIMEOUT, DEVERR_OVERFL
 FMT_NONE, FMT_BF16, FMT_F32, FMT_MXFP8, FMT_MXFP8_BF16 = 0, 1, 2, 3, 4
 STAGE_FC1_SWIGLU, STAGE_FC2 = 1, 2
 MODE_AUTO, MODE_GEMV, MODE_GEMM, MODE_SPLIT = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = 0, 1, 2, 3
 
 # every entry point declared in include/moe.h
 EXPORTS = ["moe_version", "moe_last_error_string", "moe_get_error", "moe_set_wait_limit", "moe_set_side_sms",
@@ -30,7 +32,7 @@ EXPORTS = ["moe_version", "moe_last_error_string", "moe_get_error", "moe_set_wai
            "mxfp4_to_fp8_ws", "moe_w2_mm_workspace_size", "moe_w2_mm", "moe_w2_mm_noalloc", "moe_mxfp4_mm",
            "moe_combine", "moe_cache_select", "moe_cache_fill", "moe_stage_select", "moe_w2_mm_slots",
            "moe_w2_decode_fused_workspace_size", "moe_w2_decode_fused", "moe_w2_decode_layer_workspace_size",
-           "moe_w2_decode_layer"]
+           "moe_w2_decode_layer", "moe_add_rmsnorm", "moe_route_scored", "moe_gather_mxfp8", "moe_linear"]
 W2_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -40,7 +42,7 @@ class MoEError(RuntimeError):
         self.code = code
 
 
-_P, _I, _L, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_P, _I, _L, _S, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "moe_version": (_I, []),
     "moe_last_error_string": (ctypes.c_char_p, []),
@@ -70,6 +72,10 @@ _SIGS = {
     "moe_w2_decode_layer_workspace_size": (_S, [_I, _I, _I, _I]),
     "moe_w2_decode_layer": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I,
                                  _P, _S, _P, _P]),
+    "moe_add_rmsnorm": (_I, [_P, _I, _L, _P, _I, _L, _P, _I, _F, _I, _I, _P, _L, _P, _I, _P, _P, _P]),
+    "moe_route_scored": (_I, [_P, _L, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
+    "moe_gather_mxfp8": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_linear": (_I, [_P, _L, _P, _L, _P, _I, _P, _I, _L, _I, _I, _I, _P, _I, _L, _P, _P]),
     "moe_w2_mm_slots": (_I, [_I, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _S, _P, _P]),
 }
 
@@ -271,3 +277,88 @@ def moe_w2_decode_layer(logits, x, k, codes1, scales1, codes2, scales2, H, I, id
                                      _ptr(scales2), H, I, _ptr(ids), _ptr(w), _ptr(offsets), _ptr(perm), _ptr(inv),
                                      _ptr(h), _ptr(y), _ptr(out), out_fmt, _ptr(ws), nbytes, _ptr(dev_err),
                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------- block operators
+# The formats and row strides come from the tensors: float32 is FMT_F32,
+# bfloat16 or its int16 bit patterns FMT_BF16; rows may be strided where the
+# C declaration has an ld argument.
+
+_FMT_OF = {torch.float32: FMT_F32, torch.bfloat16: FMT_BF16, torch.int16: FMT_BF16, torch.uint16: FMT_BF16}
+
+
+def _refuse(who: str, what: str):
+    raise MoEError(MOE_ERR_ARG, f"{who}: {what}")
+
+
+def _fmt(who, t) -> int:
+    if t is None:
+        return FMT_NONE
+    f = _FMT_OF.get(t.dtype)
+    if f is None:
+        _refuse(who, f"dtype {t.dtype}")
+    return f
+
+
+def _rows(who, t, T: int, cols: int) -> int:
+    """Row stride of a [T, cols] tensor whose rows are contiguous (0: no tensor)."""
+    if t is None:
+        return 0
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        _refuse(who, f"shape {tuple(t.shape)} / strides {t.stride()}, wanted contiguous rows [{T}, {cols}]")
+    return t.stride(0) if T > 1 else cols
+
+
+def _flat(who, t, n: int):
+    if t is not None and (t.numel() != n or not t.is_contiguous()):
+        _refuse(who, f"shape {tuple(t.shape)}, wanted {n} contiguous elements")
+
+
+def moe_add_rmsnorm(x, gain, eps, res=None, sum_out=None, out=None, q=None, q_scale=None, stream=None):
+    who = "moe_add_rmsnorm"
+    T, H = x.shape
+    _flat(who, gain, H)
+    _flat(who, out, T * H)
+    _flat(who, q, T * H)
+    _flat(who, q_scale, T * (H // 32))
+    if sum_out is not None and (res is None or _fmt(who, sum_out) != _fmt(who, res)):
+        _refuse(who, "sum_out needs res, in its dtype")
+    _check(lib().moe_add_rmsnorm(_ptr(x), _fmt(who, x), _rows(who, x, T, H), _ptr(res), _fmt(who, res),
+                                 _rows(who, res, T, H), _ptr(gain), _fmt(who, gain), eps, T, H, _ptr(sum_out),
+                                 _rows(who, sum_out, T, H), _ptr(out), _fmt(who, out), _ptr(q), _ptr(q_scale),
+                                 _stream(stream)))
+
+
+def moe_route_scored(logits, k, ids, w, bias=None, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1,
+                     renorm=True, scale=1.0, dev_err=None, stream=None):
+    who = "moe_route_scored"
+    T, E = logits.shape
+    _flat(who, bias, E)
+    _flat(who, ids, T * k)
+    _flat(who, w, T * k)
+    _check(lib().moe_route_scored(_ptr(logits), _rows(who, logits, T, E), _ptr(bias), T, E, k, score, n_group,
+                                  topk_group, group_top, int(bool(renorm)), scale, _ptr(ids), _ptr(w),
+                                  _ptr(dev_err), _stream(stream)))
+
+
+def moe_gather_mxfp8(x_q, x_scale, inv, k, x_perm, x_perm_scale, stream=None):
+    who = "moe_gather_mxfp8"
+    T, H = x_q.shape
+    for t, n in ((x_q, T * H), (x_scale, T * (H // 32)), (inv, T * k), (x_perm, T * k * H),
+                 (x_perm_scale, T * k * (H // 32))):
+        _flat(who, t, n)
+    _check(lib().moe_gather_mxfp8(_ptr(x_q), _ptr(x_scale), _ptr(inv), T, k, H, _ptr(x_perm), _ptr(x_perm_scale),
+                                  _stream(stream)))
+
+
+def moe_linear(x, w, out, bias=None, act=ACT_NONE, res=None, dev_err=None, stream=None):
+    who = "moe_linear"
+    T, K = x.shape
+    rows = w.shape[0]
+    N = rows // 2 if act == ACT_SWIGLU else rows
+    if _fmt(who, x) != FMT_BF16 or _fmt(who, w) != FMT_BF16 or (act == ACT_SWIGLU and rows % 2):
+        _refuse(who, "x and w are bf16; SWIGLU weights have an even number of rows")
+    _flat(who, bias, rows)
+    _check(lib().moe_linear(_ptr(x), _rows(who, x, T, K), _ptr(w), _rows(who, w, rows, K), _ptr(bias), act, _ptr(res),
+                            _fmt(who, res), _rows(who, res, T, N), T, N, K, _ptr(out), _fmt(who, out),
+                            _rows(who, out, T, N), _ptr(dev_err), _stream(stream)))

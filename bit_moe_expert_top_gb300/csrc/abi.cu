@@ -665,4 +665,87 @@ int moe_combine(const void* y, int y_fmt, const float* w, const int32_t* inv, in
                      "moe_combine");
 }
 
+// row stride of a block operator's argument: at least the row, looked at for
+// two rows or more
+static bool bad_ld(int64_t ld, int T, int cols) { return T > 1 && ld < cols; }
+static bool row_fmt(int f) { return f == MOE_FMT_BF16 || f == MOE_FMT_F32; }
+static uintptr_t fmt_align(int f) { return f == MOE_FMT_F32 ? 4 : 2; }
+
+int moe_add_rmsnorm(const void* x, int x_fmt, int64_t ldx, const void* res, int res_fmt, int64_t ldr, const void* gain,
+                    int gain_fmt, float eps, int T, int H, void* sum, int64_t lds, void* out, int out_fmt, uint8_t* q,
+                    uint8_t* q_scale, void* stream) {
+  if (T < 0 || H < 1 || H > 16384) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: bad shape (T >= 0, 1 <= H <= 16384)");
+  if (!row_fmt(x_fmt) || (res && !row_fmt(res_fmt)) || (gain && !row_fmt(gain_fmt)) || (out && !row_fmt(out_fmt)))
+    return fail(MOE_ERR_ARG, "moe_add_rmsnorm: formats are BF16 or F32");
+  if (!(eps >= 0.0f)) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: eps < 0");
+  if (T == 0) return MOE_OK;
+  if (sum && !res) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: sum without res");
+  if ((q != nullptr) != (q_scale != nullptr)) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: q and q_scale go together");
+  if (q && (H % 32 || !aligned(q, 16))) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: q needs H % 32 == 0 and 16-byte alignment");
+  if (!x || (!sum && !out && !q)) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: x NULL or no output");
+  if (!aligned(x, fmt_align(x_fmt)) || !aligned(res, fmt_align(res_fmt)) || !aligned(sum, fmt_align(res_fmt)) ||
+      !aligned(gain, fmt_align(gain_fmt)) || !aligned(out, fmt_align(out_fmt)))
+    return fail(MOE_ERR_ARG, "moe_add_rmsnorm: pointer not aligned to its elements");
+  if (bad_ld(ldx, T, H) || (res && bad_ld(ldr, T, H)) || (sum && bad_ld(lds, T, H)))
+    return fail(MOE_ERR_ARG, "moe_add_rmsnorm: row stride below H");
+  if (sum && sum == res && T > 1 && lds != ldr) return fail(MOE_ERR_ARG, "moe_add_rmsnorm: in place needs lds == ldr");
+  if (int r = check_device()) return r;
+  NormArgs a{x, x_fmt, ldx, res, res_fmt, ldr, gain, gain_fmt, eps, T, H, sum, lds, out, out_fmt, q, q_scale};
+  return cuda_status(launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)), "moe_add_rmsnorm");
+}
+
+int moe_route_scored(const float* logits, int64_t ldl, const float* bias, int T, int E, int k, int score, int n_group,
+                     int topk_group, int group_top, int renorm, float scale, int32_t* ids, float* w, uint32_t* dev_err,
+                     void* stream) {
+  if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return fail(MOE_ERR_ARG, "moe_route_scored: bad shape");
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_ARG, "moe_route_scored: score");
+  if (n_group < 1 || n_group > 32 || E % n_group || topk_group < 1 || topk_group > n_group)
+    return fail(MOE_ERR_ARG, "moe_route_scored: groups (n_group <= 32 dividing E, 1 <= topk_group <= n_group)");
+  if ((group_top != 1 && group_top != 2) || (n_group > 1 && group_top > E / n_group))
+    return fail(MOE_ERR_ARG, "moe_route_scored: group_top is 1 or 2, at most the experts of a group");
+  if (k > topk_group * (E / n_group)) return fail(MOE_ERR_ARG, "moe_route_scored: k above the experts of topk_group groups");
+  if (T == 0) return MOE_OK;
+  if (!logits || !ids || !w || !aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
+    return fail(MOE_ERR_ARG, "moe_route_scored: NULL or misaligned pointer");
+  if (bad_ld(ldl, T, E)) return fail(MOE_ERR_ARG, "moe_route_scored: ldl below E");
+  if (int r = check_device()) return r;
+  RouteArgs a{logits, ldl, bias, T, E, k, score, n_group, topk_group, group_top, renorm, scale, ids, w, dev_err};
+  return cuda_status(launch_route_scored(a, static_cast<cudaStream_t>(stream)), "moe_route_scored");
+}
+
+int moe_gather_mxfp8(const uint8_t* x_q, const uint8_t* x_scale, const int32_t* inv, int T, int k, int H,
+                     uint8_t* x_perm, uint8_t* x_perm_scale, void* stream) {
+  if (T < 0 || k < 1 || k > 32 || H < 1 || H % 32 || static_cast<int64_t>(T) * k >= (1LL << 31))
+    return fail(MOE_ERR_ARG, "moe_gather_mxfp8: bad shape (H a positive multiple of 32, k <= 32, T*k < 2^31)");
+  if (T == 0) return MOE_OK;
+  if (!x_q || !x_scale || !inv || !x_perm || !x_perm_scale || !aligned(x_q, 16) || !aligned(x_perm, 16) ||
+      !aligned(inv, 4))
+    return fail(MOE_ERR_ARG, "moe_gather_mxfp8: NULL or misaligned pointer");
+  if (int r = check_device()) return r;
+  return cuda_status(launch_gather_mxfp8(x_q, x_scale, inv, T, k, H, x_perm, x_perm_scale,
+                                         static_cast<cudaStream_t>(stream)),
+                     "moe_gather_mxfp8");
+}
+
+int moe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias, int act, const void* res,
+               int res_fmt, int64_t ldr, int T, int N, int K, void* out, int out_fmt, int64_t ldo, uint32_t* dev_err,
+               void* stream) {
+  if (T < 0 || N < 1 || K < 1 || N > (1 << 29)) return fail(MOE_ERR_ARG, "moe_linear: bad shape");
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return fail(MOE_ERR_ARG, "moe_linear: act");
+  if (!row_fmt(out_fmt) || (res && !row_fmt(res_fmt))) return fail(MOE_ERR_ARG, "moe_linear: formats are BF16 or F32");
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out || !aligned(x, 2) || !aligned(w, 2) || !aligned(bias, 4) || !aligned(res, fmt_align(res_fmt)) ||
+      !aligned(out, fmt_align(out_fmt)))
+    return fail(MOE_ERR_ARG, "moe_linear: NULL or misaligned pointer");
+  if (bad_ld(ldx, T, K) || bad_ld(ldw, act == MOE_ACT_SWIGLU ? 2 * N : N, K) || (res && bad_ld(ldr, T, N)) ||
+      bad_ld(ldo, T, N))
+    return fail(MOE_ERR_ARG, "moe_linear: row stride below the row");
+  if (res == out && (res_fmt != out_fmt || (T > 1 && ldr != ldo)))
+    return fail(MOE_ERR_ARG, "moe_linear: in place needs the same format and stride");
+  if (int r = check_device()) return r;
+  LinearArgs a{static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(w), ldw, bias, act, res, res_fmt, ldr,
+               T, N, K, out, out_fmt, ldo, dev_err, wait_limit()};
+  return cuda_status(launch_linear(a, static_cast<cudaStream_t>(stream)), "moe_linear");
+}
+
 }  // extern "C"

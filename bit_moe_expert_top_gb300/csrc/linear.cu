@@ -1,0 +1,80 @@
+// Dense matrix product with bias, activation and residual in its epilogue:
+// CUDA-core kernel for any shape, stride and alignment.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.cuh"
+#include "linear_common.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kLT = 64, kLK = 16;  // outputs per tile edge, K elements per step
+
+// One CTA per 64 tokens x 64 outputs, 4 x 4 outputs a thread (two sets of
+// sums for SwiGLU), operands staged in shared memory as fp32.
+template <bool kGlu>
+__global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
+  __shared__ float sx[kLK][kLT + 4];
+  __shared__ float sw[kGlu ? 2 : 1][kLK][kLT + 4];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int n0 = blockIdx.x * kLT;
+  for (int t0 = blockIdx.y * kLT; t0 < a.T; t0 += gridDim.y * kLT) {
+    float acc[kGlu ? 2 : 1][4][4] = {};
+    for (int k0 = 0; k0 < a.K; k0 += kLK) {
+      for (int i = tid; i < kLT * kLK; i += 256) {
+        const int r = i / kLK, kk = i % kLK;
+        const bool kin = k0 + kk < a.K;
+        sx[kk][r] = (kin && t0 + r < a.T) ? bf16_bits_to_f32(a.x[(t0 + r) * a.ldx + k0 + kk]) : 0.f;
+        const bool nin = kin && n0 + r < a.N;
+        sw[0][kk][r] = nin ? bf16_bits_to_f32(a.w[(n0 + r) * a.ldw + k0 + kk]) : 0.f;
+        if (kGlu) sw[kGlu][kk][r] = nin ? bf16_bits_to_f32(a.w[(static_cast<int64_t>(a.N) + n0 + r) * a.ldw + k0 + kk]) : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int kk = 0; kk < kLK; ++kk) {
+        float xv[4], wv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i] = sx[kk][ty * 4 + i];
+#pragma unroll
+        for (int g = 0; g < (kGlu ? 2 : 1); ++g) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) wv[i] = sw[g][kk][tx + 16 * i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[g][i][j] = fmaf(xv[i], wv[j], acc[g][i][j]);
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + ty * 4 + i, n = n0 + tx + 16 * j;
+        if (t >= a.T || n >= a.N) continue;
+        float v = acc[0][i][j] + (a.bias ? a.bias[n] : 0.f);
+        if (kGlu)
+          v = swiglu_f32(v, acc[kGlu][i][j] + (a.bias ? a.bias[a.N + n] : 0.f));
+        else
+          v = linear_act(v, a.act);
+        linear_store(a, t, n, v);
+      }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  const int gt = (a.T + kLT - 1) / kLT;
+  const dim3 grid((a.N + kLT - 1) / kLT, gt < 65535 ? gt : 65535);
+  if (a.act == MOE_ACT_SWIGLU) return launch_pdl(linear_kernel<true>, grid, dim3(256), 0, s, a);
+  return launch_pdl(linear_kernel<false>, grid, dim3(256), 0, s, a);
+}
+
+}  // namespace moe

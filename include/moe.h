@@ -510,6 +510,88 @@ MOE_API int moe_cache_fill(const int32_t* promoted, int S, int n_arrays, const v
 MOE_API int moe_combine(const void* y, int y_fmt, const float* w, const int32_t* inv,
                 int T, int k, int H, void* out, int out_fmt, void* stream);
 
+/* ------------------------------------------------------------------ block operators
+ * What stands around the routed experts in one MoE block (the pages describe
+ * the layer only; these complete the path from the residual stream to the
+ * block's output): the norm that feeds the router and the experts, the
+ * router's product and the shared expert, routing on scores, and the gather
+ * of rows that are MXFP8 already.  Forward only.  Rows may be strided (the
+ * ld* arguments, in elements: row r starts at ld*r); the elements of a row are
+ * contiguous.  For T <= 1 the ld* are not looked at.
+ *
+ * moe_add_rmsnorm: residual addition, root-mean-square norm, optional MXFP8.
+ *   y = x + res (fp32; y = x without res)
+ *   sum[t][i] = y rounded to res_fmt
+ *   n = y / sqrt(mean_i y_i^2 + eps) * gain[i], all in fp32, from the unrounded y
+ *   out[t][i] = n rounded to out_fmt
+ *   q, q_scale = MXFP8 (as moe_permute's gather, OCP MX) of n rounded to BF16,
+ *        so the codes are those of a gather that quantises a BF16 out
+ * x / res / gain in BF16 or F32; res, sum, out, q (with q_scale) and gain
+ * (NULL: ones) may each be NULL, but sum needs res, and one of sum, out, q must
+ * be there.  sum may be res itself (in place, lds == ldr); out [T][H], q
+ * [T][H], q_scale [T][H/32] are contiguous, the form the other calls read.
+ * 1 <= H <= 16384; q needs H a multiple of 32, q 16-byte aligned.  Pointers
+ * aligned to their elements; 16-byte aligned rows take the wide path.  NaN and infinite elements give
+ * what the formula gives (their row's n is NaN or 0).  T = 0 is a no-op. */
+MOE_API int moe_add_rmsnorm(const void* x, int x_fmt, int64_t ldx, const void* res, int res_fmt, int64_t ldr,
+                    const void* gain, int gain_fmt, float eps, int T, int H, void* sum, int64_t lds,
+                    void* out, int out_fmt, uint8_t* q, uint8_t* q_scale, void* stream);
+
+/* score functions and activations */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1    /* v / (1 + e^-v)                                      */
+#define MOE_ACT_GELU 2    /* v/2 (1 + erf(v / sqrt 2))                           */
+#define MOE_ACT_SWIGLU 3  /* silu(gate) * up; W has 2N rows, gate rows first (W1) */
+
+/* Top-k routing on scores: a balance bias, expert groups, weights without the
+ * bias (moe_route is the case softmax, no bias, one group, renormalised).
+ *   logits float, rows ldl apart; bias float [E], nullable
+ *   s = softmax(logits) over all E, or sigmoid(logits), fp32
+ *   c = s + bias                          the score that selects
+ *   groups: E / n_group consecutive experts each; a group's score is the sum
+ *           of its group_top (1 or 2) largest c; the topk_group groups of
+ *           largest score stay (ties to the lowest group)
+ *   ids   int32 [T][k] out: the k experts of largest c within them, by
+ *         (c desc, id asc)
+ *   w     float [T][k] out: s of those experts, over their sum where renorm
+ *         is non-zero (0 where that sum is 0), times scale
+ * A logit of -inf masks its expert: s = 0 and c below every number, whatever
+ * the bias.  A NaN logit or a NaN c does the same, ranks below -inf and sets
+ * NAN_LOGIT.  A row whose experts are all masked gives the lowest ids of the lowest
+ * groups with w = 0.  An infinite logit takes softmax weight 1 (shared with
+ * its equals).  1 <= k <= 32, E <= 1024, n_group <= 32 dividing E, group_top <=
+ * E / n_group, k <= topk_group * E / n_group.  T = 0 is a no-op. */
+MOE_API int moe_route_scored(const float* logits, int64_t ldl, const float* bias, int T, int E, int k, int score,
+                     int n_group, int topk_group, int group_top, int renorm, float scale, int32_t* ids, float* w,
+                     uint32_t* dev_err, void* stream);
+
+/* The gather of moe_permute for rows that are MXFP8 already:
+ * x_perm[inv[t*k + j]] = x_q[t] and x_perm_scale[...] = x_scale[t] for every
+ * j < k with inv >= 0 (inv as moe_permute writes it, called there with
+ * MOE_FMT_NONE).  x_q [T][H], x_scale [T][H/32], x_perm [T*k][H], x_perm_scale
+ * [T*k][H/32]; H a positive multiple of 32; x_q and x_perm 16-byte aligned. */
+MOE_API int moe_gather_mxfp8(const uint8_t* x_q, const uint8_t* x_scale, const int32_t* inv, int T, int k, int H,
+                     uint8_t* x_perm, uint8_t* x_perm_scale, void* stream);
+
+/* Dense matrix product with bias, activation and residual in its epilogue (the
+ * router's projection to fp32 logits; a shared expert's two products).
+ *   v[t][n] = sum_i x[t][i] W[n][i] + bias[n]      fp32
+ *   out[t][n] = act(v)[t][n] + res[t][n], rounded once to out_fmt
+ * x bf16 [T][K], W bf16 [N][K] (MOE_ACT_SWIGLU: [2N][K], gate rows first, and
+ * bias 2N), bias float nullable, res BF16 / F32 nullable, out BF16 / F32; rows
+ * of x, W, res, out ldx, ldw, ldr, ldo apart.  res may be out itself (same
+ * format and stride).  T >= 0, N, K >= 1, any of them odd; pointers aligned to
+ * their elements.  The tensor cores take x and W whose base and row stride are multiples of 16
+ * bytes, with K a multiple of 8 (SWIGLU: N a multiple of 16); others run on a
+ * slower CUDA-core kernel.  Sums of the fp32 output are kept in fp32 over at
+ * most 512 elements of K at a time and then added with rounding to nearest
+ * (the tensor core's own accumulation truncates). */
+MOE_API int moe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias, int act,
+               const void* res, int res_fmt, int64_t ldr, int T, int N, int K, void* out, int out_fmt, int64_t ldo,
+               uint32_t* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,91 @@
+"""What the block operators refuse, checked on the host before any device call
+(no GPU: the addresses are never read)."""
+import pytest
+import torch
+
+from tests.test_abi_exports import lib_path  # noqa: F401  (builds the library when it is missing)
+
+from bit_moe_expert_top_gb300 import _lib as L
+
+A = 4096  # an aligned address that no refused call touches
+
+
+def _norm(lib, **kw):
+    d = dict(x=A, x_fmt=L.FMT_BF16, ldx=64, res=None, res_fmt=0, ldr=0, gain=None, gain_fmt=0, eps=1e-6, T=2, H=64,
+             sum=None, lds=0, out=A, out_fmt=L.FMT_BF16, q=None, q_scale=None, stream=None)
+    d.update(kw)
+    return lib.moe_add_rmsnorm(*d.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(H=0), dict(H=16385, ldx=16385), dict(x=None), dict(out=None), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(x_fmt=L.FMT_MXFP8), dict(out_fmt=L.FMT_NONE), dict(ldx=63), dict(x=A + 1), dict(out=A + 2, out_fmt=L.FMT_F32),
+    dict(sum=A, lds=64), dict(res=A, res_fmt=7, ldr=64), dict(res=A, res_fmt=L.FMT_F32, ldr=10),
+    dict(q=A), dict(q_scale=A), dict(q=A + 8, q_scale=A), dict(H=48, q=A, q_scale=A),
+    dict(res=A, res_fmt=L.FMT_F32, ldr=64, sum=A, lds=65),
+], ids=str)
+def test_add_rmsnorm_refuses(lib_path, kw):  # noqa: F811
+    assert _norm(L.lib(), **kw) == L.MOE_ERR_ARG
+
+
+def _route(lib, **kw):
+    d = dict(logits=A, ldl=64, bias=None, T=2, E=64, k=4, score=L.SCORE_SIGMOID, n_group=8, topk_group=4, group_top=2,
+             renorm=1, scale=1.0, ids=A, w=A, dev_err=None, stream=None)
+    d.update(kw)
+    return lib.moe_route_scored(*d.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(E=0), dict(E=1025, ldl=1025, n_group=1, topk_group=1), dict(k=0), dict(k=33), dict(E=2, k=3, n_group=1, topk_group=1),
+    dict(score=2), dict(n_group=0), dict(n_group=5), dict(n_group=64, topk_group=4, group_top=1), dict(topk_group=0),
+    dict(topk_group=9), dict(group_top=0), dict(group_top=3), dict(E=8, n_group=8, group_top=2), dict(k=5, E=8, topk_group=4, group_top=1),
+    dict(logits=None), dict(ids=None), dict(w=None), dict(ldl=63), dict(logits=A + 2),
+], ids=str)
+def test_route_scored_refuses(lib_path, kw):  # noqa: F811
+    assert _route(L.lib(), **kw) == L.MOE_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(k=0), dict(H=0), dict(H=48), dict(xq=None), dict(xq=A + 8), dict(inv=None),
+                                dict(T=1 << 30, k=2)], ids=str)
+def test_gather_mxfp8_refuses(lib_path, kw):  # noqa: F811
+    d = dict(xq=A, xs=A, inv=A, T=2, k=2, H=64, xp=A, xps=A, stream=None)
+    d.update(kw)
+    assert L.lib().moe_gather_mxfp8(*d.values()) == L.MOE_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(N=0), dict(K=0), dict(act=4), dict(act=-1), dict(x=None), dict(w=None), dict(out=None), dict(x=A + 1),
+    dict(bias=A + 2), dict(out_fmt=L.FMT_MXFP8), dict(res=A, res_fmt=0), dict(ldx=63), dict(ldw=63), dict(ldo=31),
+    dict(res=A, res_fmt=L.FMT_BF16, ldr=31), dict(res=A, res_fmt=L.FMT_F32, ldr=32), dict(act=L.ACT_SWIGLU, N=1, ldw=63, ldo=32),
+], ids=str)
+def test_linear_refuses(lib_path, kw):  # noqa: F811
+    d = dict(x=A, ldx=64, w=A, ldw=64, bias=None, act=0, res=None, res_fmt=0, ldr=0, T=2, N=32, K=64, out=A,
+             out_fmt=L.FMT_BF16, ldo=32, dev_err=None, stream=None)
+    d.update(kw)
+    assert L.lib().moe_linear(*d.values()) == L.MOE_ERR_ARG
+
+
+def test_empty_batches_are_no_ops(lib_path):  # noqa: F811
+    lib = L.lib()
+    assert _norm(lib, T=0, x=None, out=None) == L.MOE_OK
+    assert _route(lib, T=0, logits=None, ids=None, w=None) == L.MOE_OK
+    assert lib.moe_gather_mxfp8(None, None, None, 0, 2, 64, None, None, None) == L.MOE_OK
+    assert lib.moe_linear(None, 0, None, 0, None, 0, None, 0, 0, 0, 8, 8, None, L.FMT_F32, 0, None, None) == L.MOE_OK
+
+
+def test_binding_refuses_tensors_it_cannot_describe(lib_path):  # noqa: F811
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(L.MoEError):  # dtype
+        L.moe_add_rmsnorm(x.double(), None, 1e-6, out=x, stream=0)
+    with pytest.raises(L.MoEError):  # a transposed output
+        L.moe_add_rmsnorm(x, None, 1e-6, out=torch.zeros(64, 4, dtype=torch.bfloat16).t(), stream=0)
+    with pytest.raises(L.MoEError):  # sum_out in another dtype than res
+        L.moe_add_rmsnorm(x, None, 1e-6, res=x, sum_out=x.float(), stream=0)
+    with pytest.raises(L.MoEError):  # elements of a row apart
+        L.moe_linear(x.t(), torch.zeros(8, 4, dtype=torch.bfloat16), torch.zeros(64, 8), stream=0)
+    with pytest.raises(L.MoEError):  # odd number of gate and up rows
+        L.moe_linear(x, torch.zeros(7, 64, dtype=torch.bfloat16), torch.zeros(4, 3), act=L.ACT_SWIGLU, stream=0)
+    with pytest.raises(L.MoEError):  # too few scales
+        L.moe_gather_mxfp8(x.view(torch.uint8)[:, :64].contiguous(), torch.zeros(4, 1, dtype=torch.uint8),
+                           torch.zeros(4, 2, dtype=torch.int32), 2, torch.zeros(8, 64, dtype=torch.uint8),
+                           torch.zeros(8, 2, dtype=torch.uint8), stream=0)
