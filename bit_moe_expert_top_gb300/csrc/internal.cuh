@@ -205,6 +205,9 @@ struct LinearArgs {
   long long wait;     // bounded-wait limit in SM clock cycles
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+// on the tensor cores (linear_tc.cu): K, strides and addresses that TMA takes
+bool linear_tc_supported(const LinearArgs& a);
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s);
 
 // ---- diagnostics (diag.cu)
 // One warp waits with the pipelines' bounded wait, limit `cycles`, on a
