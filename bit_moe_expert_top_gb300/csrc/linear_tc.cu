@@ -221,6 +221,45 @@ MOE_D void tm_st(uint32_t t, const uint32_t (&r)[16]) { tm_st16(t, r); }
 MOE_D void tm_st(uint32_t t, const uint32_t (&r)[32]) { tm_st32(t, r); }
 
 // ------------------------------------------------------------------ epilogue
+// M outputs of this lane, at rows (tokens) t0, t0 + step, ...: the residual is
+// added and the sums are stored.  cnt > 0 of them are inside T.  The loads
+// are issued together (rows past the end read the last one again): with a
+// branch per load each waited for its own and the epilogue set the pace (838
+// us instead of 342 us at T 16384, N 7168, K 2048 with a bf16 residual).
+template <int M>
+MOE_D void emit_rows(const LinearArgs& a, float (&v)[M], int64_t t0, int step, int cnt, int64_t n) {
+  if (a.res) {
+    const int64_t ld = a.ldr * step;
+    if (a.res_fmt == MOE_FMT_F32) {
+      const float* p = static_cast<const float*>(a.res) + t0 * a.ldr + n;
+      float r[M];
+#pragma unroll
+      for (int c = 0; c < M; ++c) r[c] = p[(c < cnt ? c : cnt - 1) * ld];
+#pragma unroll
+      for (int c = 0; c < M; ++c) v[c] += r[c];
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(a.res) + t0 * a.ldr + n;
+      uint16_t r[M];
+#pragma unroll
+      for (int c = 0; c < M; ++c) r[c] = p[(c < cnt ? c : cnt - 1) * ld];
+#pragma unroll
+      for (int c = 0; c < M; ++c) v[c] += bf16_bits_to_f32(r[c]);
+    }
+  }
+  const int64_t ld = a.ldo * step;
+  if (a.out_fmt == MOE_FMT_F32) {
+    float* p = static_cast<float*>(a.out) + t0 * a.ldo + n;
+#pragma unroll
+    for (int c = 0; c < M; ++c)
+      if (c < cnt) p[c * ld] = v[c];
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + t0 * a.ldo + n;
+#pragma unroll
+    for (int c = 0; c < M; ++c)
+      if (c < cnt) p[c * ld] = f32_to_bf16_rne(v[c]);
+  }
+}
+
 // This lane's outputs of CW columns (tokens t0 ..): bias, activation,
 // residual, store.  n: the lane's output feature (nok: inside N).
 template <int CW>
@@ -230,50 +269,33 @@ MOE_D void emit(const LinearArgs& a, float (&v)[CW], int64_t t0, int64_t n, bool
   if (a.act == MOE_ACT_SWIGLU) {
     // lanes 0-15: gate rows, lanes 16-31: the up rows of the same outputs.
     // Of columns (c, c + 1) the low half finishes c, the high half c + 1.
-    const bool hi = lane >= 16;
+    const int hi = lane >> 4;
     float bg = 0.f, bu = 0.f;
     if (a.bias && nok) {
       bg = __ldg(a.bias + n);
       bu = __ldg(a.bias + a.N + n);
     }
+    float u[CW / 2];
 #pragma unroll
     for (int c = 0; c < CW; c += 2) {
       const float other = __shfl_xor_sync(0xffffffffu, hi ? v[c] : v[c + 1], 16);
-      const float g = (hi ? other : v[c]) + bg, u = (hi ? v[c + 1] : other) + bu;
-      const int cc = c + (hi ? 1 : 0);
-      if (nok && cc < nc) linear_store(a, t0 + cc, n, swiglu_f32(g, u));
+      u[c / 2] = swiglu_f32((hi ? other : v[c]) + bg, (hi ? v[c + 1] : other) + bu);
     }
+    const int cnt = (nc - hi + 1) / 2;
+    if (nok && cnt > 0) emit_rows<CW / 2>(a, u, t0 + hi, 2, cnt, n);
     return;
   }
   const float b = (a.bias && nok) ? __ldg(a.bias + n) : 0.f;
 #pragma unroll
-  for (int c = 0; c < CW; ++c) v[c] = linear_act(v[c] + b, a.act);
-  if (!nok) return;
-  if (a.res) {
-    float r[CW];
-    if (a.res_fmt == MOE_FMT_F32) {
-      const float* p = static_cast<const float*>(a.res) + t0 * a.ldr + n;
+  for (int c = 0; c < CW; ++c) v[c] += b;
+  if (a.act == MOE_ACT_SILU) {
 #pragma unroll
-      for (int c = 0; c < CW; ++c) r[c] = c < nc ? p[c * a.ldr] : 0.f;
-    } else {
-      const uint16_t* p = static_cast<const uint16_t*>(a.res) + t0 * a.ldr + n;
+    for (int c = 0; c < CW; ++c) v[c] = silu_f32(v[c]);
+  } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
-      for (int c = 0; c < CW; ++c) r[c] = c < nc ? bf16_bits_to_f32(p[c * a.ldr]) : 0.f;
-    }
-#pragma unroll
-    for (int c = 0; c < CW; ++c) v[c] += r[c];
+    for (int c = 0; c < CW; ++c) v[c] = gelu_f32(v[c]);
   }
-  if (a.out_fmt == MOE_FMT_F32) {
-    float* p = static_cast<float*>(a.out) + t0 * a.ldo + n;
-#pragma unroll
-    for (int c = 0; c < CW; ++c)
-      if (c < nc) p[c * a.ldo] = v[c];
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + t0 * a.ldo + n;
-#pragma unroll
-    for (int c = 0; c < CW; ++c)
-      if (c < nc) p[c * a.ldo] = f32_to_bf16_rne(v[c]);
-  }
+  if (nok) emit_rows<CW>(a, v, t0, 1, nc, n);
 }
 
 template <int CG, int NT>
