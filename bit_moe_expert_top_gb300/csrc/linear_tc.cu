@@ -2,7 +2,7 @@
 // the tensor cores (tcgen05, bf16 operands, fp32 accumulators in TMEM).
 //
 // A tile is 128 weight rows per CTA (TMEM lane = weight row = output feature)
-// times NT tokens (TMEM column = token): D = W_tile . X_tile^T, so a warp of
+// times nt tokens (TMEM column = token): D = W_tile . X_tile^T, so a warp of
 // the epilogue holds 32 consecutive outputs of one token in every register
 // and reads and writes them as one coalesced piece.  CG = 2: a pair of CTAs
 // forms one 256-row MMA (cta_group::2), each holding its own 128 weight rows
@@ -16,17 +16,26 @@
 //               128-byte swizzle
 //   warp 1      MMA issue (CG = 2: in the pair's first CTA) and TMEM allocation
 //   warps 2-9   epilogue, two warps per TMEM lane quarter, each on its half of
-//               the tile's columns
+//               the tile's columns: CW columns at a time through a private
+//               shared tile, so that the residual comes in and the outputs go
+//               out in 16-byte pieces.  Two-byte accesses straight from the
+//               registers took 3200 cycles per 32 columns when all CTAs
+//               stored at once; TMA copies of such tiles took from the TMA
+//               unit what the ring needs (397 us instead of 331 at T 16384,
+//               N 7168, K 2048 with a bf16 residual)
 //
 // The accumulator is double-buffered in TMEM.  For fp32 outputs the MMA
-// accumulates at most P.chunk stages (512 elements of K) into one buffer;
-// the epilogue warps add the buffers into a running sum, also in TMEM, with
-// rounding to nearest: the tensor core truncates when it accumulates, which
-// at K = 4096 alone would put the result 4e-6 off.
+// accumulates at most P.chunk stages (512 elements of K) into one buffer and
+// the epilogue warps add the buffers up in registers, with rounding to
+// nearest: the tensor core truncates when it accumulates, which at K = 4096
+// alone would put the result 4e-6 off.
 //
-// split > 1 (CG = 1): the CTAs of a cluster take consecutive parts of K for
-// one tile, leave their partial sums in shared memory, and each adds up its
-// share of the columns over the cluster in rank order (no atomics).
+// split > 1: the CTAs (pairs) of a cluster take consecutive parts of K of
+// one tile; each owns a share of the columns, receives the others' partial
+// sums of it (st.async into its shared memory, counted by an mbarrier) and
+// adds the parts up in rank order (no atomics).  Against partial sums left in
+// shared memory and read by their owner between two cluster barriers, the end
+// of a decode-sized call went from 6200 to about 2000 cycles.
 //
 // Every mbarrier wait is bounded (MOE_DEVERR_TIMEOUT).
 #include <cuda.h>
@@ -43,28 +52,26 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 320;
-constexpr int kBK = 64;          // K elements per stage: one 128-byte swizzled row
+constexpr int kBK = 64;            // K elements per stage: one 128-byte swizzled row
 constexpr int kATile = 128 * kBK * 2;
-constexpr int kChunk = 8;        // stages per accumulation of an fp32 output (512 of K)
-constexpr int kCtl = 1024;       // barriers and flags
-constexpr int kSmemMax = 232448;
-
-template <int CG, int NT>
-constexpr int stage_bytes() { return kATile + NT / CG * kBK * 2; }
-template <int CG, int NT>
-constexpr int num_stages() {
-  constexpr int n = (kSmemMax - kCtl - 1024) / stage_bytes<CG, NT>();
-  return n < 12 ? n : 12;
-}
-template <int CG, int NT>
-constexpr int smem_bytes() { return kCtl + 1024 + num_stages<CG, NT>() * stage_bytes<CG, NT>(); }
+constexpr int kChunk = 8;          // stages per accumulation of an fp32 output (512 of K)
+constexpr int kCtl = 1024;         // barriers and flags
+constexpr int kMaxStages = 12;
+constexpr int kSmemMax = 232448;   // one CTA per SM
+constexpr int kSmemHalf = 115712;  // two
 
 struct TcParams {
   LinearArgs a;
+  int nt;                       // tokens per tile, a multiple of 16 (CG = 2: 32)
   int mblocks, tblocks, tiles;  // row blocks (128 * CG rows), token blocks, their product
   int kblocks, chunk;           // stages of K, stages per accumulation
-  int split;                    // CTAs of a cluster along K (CG = 1)
+  int split;                    // parts of K, one CTA (pair) of a cluster each
   int mfast;                    // neighbouring tiles share their tokens (1) or their weight rows (0)
+  int stages, stage_bytes;      // ring
+  uint32_t cols;                // TMEM columns
+  int vec_io;                   // out (and res) rows take 16-byte accesses
+  int stg_off, stg;             // epilogue tiles: offset behind the ring, bytes of one warp's
+  int recv_off, recv_own;       // split: receive buffer behind the ring, or (recv_own = 0) the ring itself
 };
 
 // ------------------------------------------------------------------ PTX of CTA pairs and clusters
@@ -73,18 +80,18 @@ MOE_D uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-MOE_D void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
+MOE_D void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+MOE_D void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 MOE_D uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-MOE_D float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// Two floats to a CTA of the cluster, counted by that CTA's mbarrier.
+MOE_D void st_async_f32x2(uint32_t addr, float x, float y, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+               "f"(x), "f"(y), "r"(bar)
+               : "memory");
 }
 MOE_D void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -152,14 +159,14 @@ MOE_D void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t
         "l"(ad), "l"(bd), "r"(idesc), "r"(accum)
         : "memory");
 }
-// Arrives on the barrier (CG = 2: on that of both CTAs) when the MMAs issued so far are done.
+// Arrives on the barrier (CG = 2: on those of the CTAs in `mask`) when the MMAs issued so far are done.
 template <int CG>
-MOE_D void mma_commit(uint64_t* bar) {
+MOE_D void mma_commit(uint64_t* bar, uint16_t mask) {
   if (CG == 2)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(mask)
         : "memory");
   else
     umma_commit_to(bar);
@@ -187,23 +194,13 @@ MOE_D void tm_relinquish_cg() {
     tm_relinquish();
 }
 
-// CW consecutive TMEM columns of this thread's lane.
-MOE_D void tm_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
+// 16 consecutive TMEM columns of this thread's lane.
 MOE_D void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-MOE_D void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 MOE_D void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -213,105 +210,229 @@ MOE_D void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-MOE_D void tm_ld(uint32_t t, uint32_t (&r)[8]) { tm_ld8(t, r); }
-MOE_D void tm_ld(uint32_t t, uint32_t (&r)[16]) { tm_ld16(t, r); }
-MOE_D void tm_ld(uint32_t t, uint32_t (&r)[32]) { tm_ld32(t, r); }
-MOE_D void tm_st(uint32_t t, const uint32_t (&r)[8]) { tm_st8(t, r); }
-MOE_D void tm_st(uint32_t t, const uint32_t (&r)[16]) { tm_st16(t, r); }
-MOE_D void tm_st(uint32_t t, const uint32_t (&r)[32]) { tm_st32(t, r); }
 
 // ------------------------------------------------------------------ epilogue
-// M outputs of this lane, at rows (tokens) t0, t0 + step, ...: the residual is
-// added and the sums are stored.  cnt > 0 of them are inside T.  The loads
-// are issued together (rows past the end read the last one again): with a
-// branch per load each waited for its own and the epilogue set the pace (838
-// us instead of 342 us at T 16384, N 7168, K 2048 with a bf16 residual).
-template <int M>
-MOE_D void emit_rows(const LinearArgs& a, float (&v)[M], int64_t t0, int step, int cnt, int64_t n) {
-  if (a.res) {
-    const int64_t ld = a.ldr * step;
-    if (a.res_fmt == MOE_FMT_F32) {
-      const float* p = static_cast<const float*>(a.res) + t0 * a.ldr + n;
-      float r[M];
-#pragma unroll
-      for (int c = 0; c < M; ++c) r[c] = p[(c < cnt ? c : cnt - 1) * ld];
-#pragma unroll
-      for (int c = 0; c < M; ++c) v[c] += r[c];
-    } else {
-      const uint16_t* p = static_cast<const uint16_t*>(a.res) + t0 * a.ldr + n;
-      uint16_t r[M];
-#pragma unroll
-      for (int c = 0; c < M; ++c) r[c] = p[(c < cnt ? c : cnt - 1) * ld];
-#pragma unroll
-      for (int c = 0; c < M; ++c) v[c] += bf16_bits_to_f32(r[c]);
-    }
-  }
-  const int64_t ld = a.ldo * step;
-  if (a.out_fmt == MOE_FMT_F32) {
-    float* p = static_cast<float*>(a.out) + t0 * a.ldo + n;
-#pragma unroll
-    for (int c = 0; c < M; ++c)
-      if (c < cnt) p[c * ld] = v[c];
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + t0 * a.ldo + n;
-#pragma unroll
-    for (int c = 0; c < M; ++c)
-      if (c < cnt) p[c * ld] = f32_to_bf16_rne(v[c]);
-  }
+// e^x and 1 / x by the hardware's approximations (2 ulp and 1 ulp; subnormal
+// results are zero).
+MOE_D float exp_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.442695041f));
+  return r;
+}
+MOE_D float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// silu with one Newton step on the quotient, as silu_fast.
+MOE_D float silu_tc(float g) {
+  const float d = fminf(1.0f + exp_fast(-g), 1e38f);
+  const float r = rcp_fast(d), q = g * r;
+  return fmaf(fmaf(-q, d, g), r, q);
+}
+// GELU v/2 (1 + erf(v / sqrt 2)) with erf by Abramowitz and Stegun 7.1.26
+// (|error| <= 1.5e-7): erff took 5.6 us of a 20 us call here.
+MOE_D float gelu_tc(float v) {
+  const float z = fabsf(v) * 0.70710678f;
+  const float t = rcp_fast(fmaf(0.3275911f, z, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float h = 0.5f * v * (p * t * exp_fast(-z * z));  // v/2 (1 - erf z)
+  return v < 0.f ? h : v - h;
 }
 
-// This lane's outputs of CW columns (tokens t0 ..): bias, activation,
-// residual, store.  n: the lane's output feature (nok: inside N).
-template <int CW>
-MOE_D void emit(const LinearArgs& a, float (&v)[CW], int64_t t0, int64_t n, bool nok, int lane) {
-  if (t0 >= a.T) return;  // warp-uniform
-  const int nc = a.T - t0 < CW ? static_cast<int>(a.T - t0) : CW;
-  if (a.act == MOE_ACT_SWIGLU) {
-    // lanes 0-15: gate rows, lanes 16-31: the up rows of the same outputs.
-    // Of columns (c, c + 1) the low half finishes c, the high half c + 1.
-    const int hi = lane >> 4;
+// Bias and activation of this lane's CW columns.  Without SwiGLU output j of
+// the lane is column j; with it lanes 0-15 hold gate rows and lanes 16-31 the
+// up rows of the same outputs: of columns (2j, 2j + 1) the low half finishes
+// the first and the high half the second, so output j is column 2j + lane/16.
+// n: the lane's output feature (nok: inside N).
+template <int CW, bool GLU>
+MOE_D void activate(const LinearArgs& a, float (&v)[CW], float (&o)[GLU ? CW / 2 : CW], int64_t n, bool nok, int lane) {
+  if constexpr (GLU) {
+    const bool hi = lane >= 16;
     float bg = 0.f, bu = 0.f;
     if (a.bias && nok) {
       bg = __ldg(a.bias + n);
       bu = __ldg(a.bias + a.N + n);
     }
-    float u[CW / 2];
 #pragma unroll
-    for (int c = 0; c < CW; c += 2) {
-      const float other = __shfl_xor_sync(0xffffffffu, hi ? v[c] : v[c + 1], 16);
-      u[c / 2] = swiglu_f32((hi ? other : v[c]) + bg, (hi ? v[c + 1] : other) + bu);
+    for (int c = 0; c < CW / 2; ++c) {
+      const float other = __shfl_xor_sync(0xffffffffu, hi ? v[2 * c] : v[2 * c + 1], 16);
+      o[c] = silu_tc((hi ? other : v[2 * c]) + bg) * ((hi ? v[2 * c + 1] : other) + bu);
     }
-    const int cnt = (nc - hi + 1) / 2;
-    if (nok && cnt > 0) emit_rows<CW / 2>(a, u, t0 + hi, 2, cnt, n);
-    return;
+  } else {
+    const float b = (a.bias && nok) ? __ldg(a.bias + n) : 0.f;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) o[c] = v[c] + b;
+    if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int c = 0; c < CW; ++c) o[c] = silu_tc(o[c]);
+    } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int c = 0; c < CW; ++c) o[c] = gelu_tc(o[c]);
+    }
   }
-  const float b = (a.bias && nok) ? __ldg(a.bias + n) : 0.f;
-#pragma unroll
-  for (int c = 0; c < CW; ++c) v[c] += b;
-  if (a.act == MOE_ACT_SILU) {
-#pragma unroll
-    for (int c = 0; c < CW; ++c) v[c] = silu_f32(v[c]);
-  } else if (a.act == MOE_ACT_GELU) {
-#pragma unroll
-    for (int c = 0; c < CW; ++c) v[c] = gelu_f32(v[c]);
-  }
-  if (nok) emit_rows<CW>(a, v, t0, 1, nc, n);
 }
 
-template <int CG, int NT>
-__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
+template <int SZ>
+struct Elem {
+  using type = uint16_t;
+};
+template <>
+struct Elem<4> {
+  using type = float;
+};
+MOE_D float widen(float x) { return x; }
+MOE_D float widen(uint16_t x) { return bf16_bits_to_f32(x); }
+MOE_D void narrow(float* p, float v) { *p = v; }
+MOE_D void narrow(uint16_t* p, float v) { asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(*p) : "f"(v)); }
+
+// M outputs of this lane, at rows (tokens) t0, t0 + step, ...: the residual is
+// added and the sums are stored.  cnt > 0 of them are inside T.  The loads
+// are issued together (rows past the end read the last one again): with a
+// branch per load each waited for its own.
+template <int M, typename E>
+MOE_D void add_rows(const E* p, int64_t ld, int cnt, float (&v)[M]) {
+  E r[M];
+#pragma unroll
+  for (int c = 0; c < M; ++c) r[c] = p[(c < cnt ? c : cnt - 1) * ld];
+#pragma unroll
+  for (int c = 0; c < M; ++c) v[c] += widen(r[c]);
+}
+template <int M, typename E>
+MOE_D void store_rows(E* p, int64_t ld, int cnt, const float (&v)[M]) {
+#pragma unroll
+  for (int c = 0; c < M; ++c) {
+    E e;
+    narrow(&e, v[c]);
+    if (c < cnt) p[c * ld] = e;
+  }
+}
+template <int M>
+MOE_D void emit_rows(const LinearArgs& a, float (&v)[M], int64_t t0, int step, int cnt, int64_t n) {
+  if (a.res) {
+    if (a.res_fmt == MOE_FMT_F32)
+      add_rows<M>(static_cast<const float*>(a.res) + t0 * a.ldr + n, a.ldr * step, cnt, v);
+    else
+      add_rows<M>(static_cast<const uint16_t*>(a.res) + t0 * a.ldr + n, a.ldr * step, cnt, v);
+  }
+  if (a.out_fmt == MOE_FMT_F32)
+    store_rows<M>(static_cast<float*>(a.out) + t0 * a.ldo + n, a.ldo * step, cnt, v);
+  else
+    store_rows<M>(static_cast<uint16_t*>(a.out) + t0 * a.ldo + n, a.ldo * step, cnt, v);
+}
+
+// nc <= CW columns (tokens t0 ..) of this lane, straight to memory.
+template <int CW>
+MOE_D void emit(const LinearArgs& a, float (&v)[CW], int64_t t0, int nc, int64_t n, bool nok, int lane) {
+  if (a.act == MOE_ACT_SWIGLU) {
+    float o[CW / 2];
+    activate<CW, true>(a, v, o, n, nok, lane);
+    const int hi = lane >> 4, cnt = (nc - hi + 1) / 2;
+    if (nok && cnt > 0) emit_rows<CW / 2>(a, o, t0 + hi, 2, cnt, n);
+  } else {
+    float o[CW];
+    activate<CW, false>(a, v, o, n, nok, lane);
+    if (nok) emit_rows<CW>(a, o, t0, 1, nc, n);
+  }
+}
+
+// A warp's tile [CW tokens][W features] of out or res moves in 16-byte pieces,
+// lane l taking pieces l, l + 32, ...; f is called with the piece's number,
+// the address of its first element and how many of its elements lie inside N
+// (0: none, or the token is past T).
+template <typename E, int CW, int W, typename P, typename F>
+MOE_D void for_pieces(const LinearArgs& a, P* base, int64_t ld, int64_t t0, int n0, int lane, F&& f) {
+  constexpr int kPer = 16 / sizeof(E);   // elements of a piece
+  constexpr int kRow = W / kPer;         // pieces of a row
+  constexpr int kPieces = CW * kRow;
+#pragma unroll
+  for (int i = 0; i < (kPieces + 31) / 32; ++i) {
+    const int p = lane + 32 * i;
+    const int64_t t = t0 + p / kRow;
+    const int n = n0 + p % kRow * kPer;
+    int in = t < a.T && p < kPieces ? a.N - n : 0;
+    in = in < 0 ? 0 : (in > kPer ? kPer : in);
+    f(i, p, base + t * ld + n, in);
+  }
+}
+
+// The residual of one step into registers (issued a step ahead of its use).
+template <typename E, int CW, int W>
+MOE_D void load_res(const LinearArgs& a, uint4 (&r)[CW / 4], int64_t t0, int n0, int lane) {
+  for_pieces<E, CW, W>(a, static_cast<const E*>(a.res), a.ldr, t0, n0, lane, [&](int i, int, const E* src, int in) {
+    if (in == 16 / sizeof(E)) {
+      r[i] = *reinterpret_cast<const uint4*>(src);
+    } else if (in > 0) {
+      E e[16 / sizeof(E)];
+#pragma unroll
+      for (int k = 0; k < 16 / static_cast<int>(sizeof(E)); ++k) e[k] = k < in ? src[k] : E(0);
+      r[i] = *reinterpret_cast<const uint4*>(e);
+    }
+  });
+}
+template <typename E, int CW, int W, int M>
+MOE_D void add_res(const uint4 (&rr)[CW / 4], uint8_t* tile, float (&o)[M], int lane) {
+  constexpr int kPieces = CW * W * static_cast<int>(sizeof(E)) / 16;
+#pragma unroll
+  for (int i = 0; i < (kPieces + 31) / 32; ++i) reinterpret_cast<uint4*>(tile)[lane + 32 * i] = rr[i];
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < M; ++c) o[c] += widen(reinterpret_cast<const E*>(tile)[32 * c + lane]);
+}
+
+// CW columns of this warp through its shared tile: v, the residual's pieces
+// rr -> out.  `next` is called when rr may be filled again.  Element c of a
+// lane sits at 32 c + lane of the tile (SwiGLU: (2c + lane/16) * 16 + lane%16,
+// the same).
+template <int CW, bool F32, bool GLU, typename N>
+MOE_D void emit_tile(const LinearArgs& a, float (&v)[CW], const uint4 (&rr)[CW / 4], N&& next, uint8_t* tile, int64_t t0,
+                     int n0, bool nok, int lane) {
+  constexpr int W = GLU ? 16 : 32, M = GLU ? CW / 2 : CW;
+  using E = typename Elem<F32 ? 4 : 2>::type;
+  float o[M];
+  activate<CW, GLU>(a, v, o, n0 + lane % W, nok, lane);
+  if (a.res) {
+    if (a.res_fmt == MOE_FMT_F32)
+      add_res<float, CW, W>(rr, tile, o, lane);
+    else
+      add_res<uint16_t, CW, W>(rr, tile, o, lane);
+    next();
+    __syncwarp();
+  }
+#pragma unroll
+  for (int c = 0; c < M; ++c) {
+    E e;
+    narrow(&e, o[c]);
+    reinterpret_cast<E*>(tile)[32 * c + lane] = e;
+  }
+  __syncwarp();
+  for_pieces<E, CW, W>(a, static_cast<E*>(a.out), a.ldo, t0, n0, lane, [&](int, int p, E* dst, int in) {
+    if (in == 16 / sizeof(E)) {
+      *reinterpret_cast<uint4*>(dst) = reinterpret_cast<const uint4*>(tile)[p];
+    } else if (in > 0) {
+      for (int k = 0; k < in; ++k) dst[k] = reinterpret_cast<const E*>(tile)[p * (16 / sizeof(E)) + k];
+    }
+  });
+  __syncwarp();
+}
+
+// NT: most tokens a tile of this instance has (nt <= NT); SUM: fp32 outputs
+// (K accumulated in several chunks, NT / 2 registers of sums), else bf16.
+template <int CG, int NT, bool SUM>
+__global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                                 const __grid_constant__ CUtensorMap tm_x,
                                                                 const __grid_constant__ TcParams P) {
-  constexpr int kStage = stage_bytes<CG, NT>();
-  constexpr int ST = num_stages<CG, NT>();
-  constexpr uint32_t kCols = NT >= 128 ? 512 : 4 * NT;  // two accumulators and (NT <= 128) the running sum
-  constexpr int CW = NT / 2 < 32 ? NT / 2 : 32;
+  constexpr int CW = (CG == 2 && !SUM) ? 32 : 16;  // columns per epilogue step
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [ST] stage landed (CG = 2: both CTAs' halves, on the first)
-  uint64_t* empty = full + ST;                          // [ST] the stage's MMAs done
-  uint64_t* acc_full = empty + ST;                      // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);  // [stage] landed (CG = 2: both CTAs' halves, on the first)
+  uint64_t* empty = full + kMaxStages;                  // [stage] its MMAs done
+  uint64_t* acc_full = empty + kMaxStages;              // [2]
   uint64_t* acc_empty = acc_full + 2;                   // [2] read by 8 warps per CTA (CG = 2: on the first)
-  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* recv = acc_empty + 2;                       // the parts of this CTA's columns landed
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(recv + 1);
   const uint32_t base = smem_u32(smem);
   const uint32_t tiles_off = ((base + kCtl + 1023u) & ~1023u) - base;
   uint8_t* stages = smem + tiles_off;
@@ -319,14 +440,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
   const LinearArgs& a = P.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool glu = a.act == MOE_ACT_SWIGLU;
-  const uint32_t rank = (CG == 2 || P.split > 1) ? cluster_rank() : 0;
-  const int csize = CG == 2 ? 2 : P.split;
+  const int ST = P.stages, kStage = P.stage_bytes, nt = P.nt;
+  const int csize = CG * P.split;
+  const uint32_t rank = csize > 1 ? cluster_rank() : 0;
+  const int side = CG == 2 ? static_cast<int>(rank & 1) : 0;  // CTA of the pair
+  const int kpart = static_cast<int>(rank) / CG;
+  const bool lead = side == 0;
   const int unit = blockIdx.x / csize, units = gridDim.x / csize;  // the cluster walks tiles unit, unit + units, ...
-  const int kb0 = CG == 2 ? 0 : static_cast<int>(static_cast<int64_t>(P.kblocks) * rank / P.split);
-  const int kb1 = CG == 2 ? P.kblocks : static_cast<int>(static_cast<int64_t>(P.kblocks) * (rank + 1) / P.split);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * kpart / P.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (kpart + 1) / P.split);
   const int nchunk = (kb1 - kb0 + P.chunk - 1) / P.chunk;
 
   if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_w) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_x) : "memory");
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -335,15 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 8 * CG);
     }
+    mbar_init(recv, 1);
     fence_barrier_init();
+    if (P.split > 1) mbar_arrive_expect_tx(recv, nt * 512);
   }
   if (warp == 1) {
-    tm_alloc_cg<CG>(tmem_s, kCols);
+    tm_alloc_cg<CG>(tmem_s, P.cols);
     tm_relinquish_cg<CG>();
   }
   tm_fence_before();
   __syncthreads();
-  if (csize > 1) cluster_sync_all();
+  if (csize > 1) {
+    cluster_arrive();
+    cluster_wait();
+  }
   tm_fence_after();
   const uint32_t tmem = *tmem_s;
   pdl_wait();
@@ -358,158 +490,256 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
       tb = tile - mb * P.tblocks;
     }
   };
+  // split with the ring as receive buffer: every CTA's MMAs are done before a part is sent
+  auto ring_free = [&]() {
+    if (P.split > 1 && !P.recv_own) {
+      cluster_arrive();
+      cluster_wait();
+    }
+  };
 
-  if (warp == 0 && lane == 0) {  // ---------------------------------------- TMA
-    int it = 0;
-    bool ok = true;
-    for (int tile = unit; ok && tile < P.tiles; tile += units) {
-      int mb, tb;
-      tile_of(tile, mb, tb);
-      const int rb = mb * CG + (CG == 2 ? static_cast<int>(rank) : 0);          // 128-row block of this CTA
-      const int tok = tb * NT + (CG == 2 ? static_cast<int>(rank) * (NT / 2) : 0);  // its first token
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const int s = it % ST;
-        ok = mbar_wait(&empty[s], ((it / ST) & 1) ^ 1, a.wait);
-        if (!ok) break;
-        const uint32_t dst = smem_u32(stages + s * kStage);
-        uint32_t bar = smem_u32(&full[s]);
-        if (rank == 0 || CG == 1) mbar_arrive_expect_tx(&full[s], CG * kStage);
-        if (CG == 2) bar = map_rank(bar, 0);
-        if (glu)
-          tma_4d<CG>(dst, &tm_w, kb * kBK, 0, 0, rb * 4, bar);
-        else
-          tma_2d<CG>(dst, &tm_w, kb * kBK, rb * 128, bar);
-        tma_2d<CG>(dst + kATile, &tm_x, kb * kBK, tok, bar);
+  if (warp == 0) {  // ------------------------------------------------------ TMA
+    if (lane == 0) {
+      int s = 0, ph = 1, it = 0;
+      bool ok = true;
+      for (int tile = unit; ok && tile < P.tiles; tile += units) {
+        int mb, tb;
+        tile_of(tile, mb, tb);
+        const int rb = mb * CG + side;              // 128-row block of this CTA
+        const int tok = tb * nt + side * (nt / 2);  // its first token
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          ok = mbar_wait(&empty[s], ph, a.wait);
+          if (!ok) break;
+          const uint32_t dst = smem_u32(stages + s * kStage);
+          uint32_t bar = smem_u32(&full[s]);
+          if (lead) mbar_arrive_expect_tx(&full[s], CG * kStage);
+          if (CG == 2) bar = map_rank(bar, rank & ~1u);
+          if (glu)
+            tma_4d<CG>(dst, &tm_w, kb * kBK, 0, 0, rb * 4, bar);
+          else
+            tma_2d<CG>(dst, &tm_w, kb * kBK, rb * 128, bar);
+          tma_2d<CG>(dst + kATile, &tm_x, kb * kBK, tok, bar);
+          if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
+        if (lead)  // the copies in flight land before the CTA ends
+          for (int i = it > ST ? it - ST : 0; i < it; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, a.wait);
       }
     }
-    if (!ok) {
-      set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
-      if (rank == 0 || CG == 1)  // the copies in flight land before the CTA ends
-        for (int i = it > ST ? it - ST : 0; i < it; ++i) mbar_wait(&full[i % ST], (i / ST) & 1, a.wait);
-    }
-  } else if (warp == 1 && lane == 0 && (CG == 1 || rank == 0)) {  // -------- MMA
-    const uint32_t idesc = idesc_bf16_mn(128 * CG, NT);
-    int it = 0, ai = 0;
-    bool ok = true;
-    for (int tile = unit; ok && tile < P.tiles; tile += units) {
-      for (int kc = kb0; ok && kc < kb1; kc += P.chunk, ++ai) {
-        const int b = ai & 1;
-        ok = CG == 2 ? mbar_wait_cluster(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait)
-                     : mbar_wait(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait);
-        if (!ok) break;
-        tm_fence_after();
-        const uint32_t d = tmem + b * NT;
-        const int ke = kc + P.chunk < kb1 ? kc + P.chunk : kb1;
-        for (int kb = kc; kb < ke; ++kb, ++it) {
-          const int s = it % ST;
-          ok = mbar_wait(&full[s], (it / ST) & 1, a.wait);
+    __syncwarp();
+    ring_free();
+  } else if (warp == 1) {  // ----------------------------------------------- MMA
+    if (lane == 0 && lead) {
+      const uint32_t idesc = idesc_bf16_mn(128 * CG, nt);
+      const uint16_t mask = static_cast<uint16_t>(3u << (rank & ~1u));
+      int s = 0, ph = 0, ai = 0;
+      bool ok = true;
+      for (int tile = unit; ok && tile < P.tiles; tile += units) {
+        for (int kc = kb0; ok && kc < kb1; kc += P.chunk, ++ai) {
+          const int b = ai & 1;
+          ok = CG == 2 ? mbar_wait_cluster(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait)
+                       : mbar_wait(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait);
           if (!ok) break;
           tm_fence_after();
-          const uint64_t ad = desc_sw128(smem_u32(stages + s * kStage));
-          const uint64_t bd = desc_sw128(smem_u32(stages + s * kStage + kATile));
+          const uint32_t d = tmem + b * nt;
+          const int ke = kc + P.chunk < kb1 ? kc + P.chunk : kb1;
+          for (int kb = kc; kb < ke; ++kb) {
+            ok = mbar_wait(&full[s], ph, a.wait);
+            if (!ok) break;
+            tm_fence_after();
+            const uint64_t ad = desc_sw128(smem_u32(stages + s * kStage));
+            const uint64_t bd = desc_sw128(smem_u32(stages + s * kStage + kATile));
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)  // 16 elements of K = 32 bytes inside the swizzled row
-            mma_ss<CG>(d, ad + 2 * k, bd + 2 * k, idesc, (kb > kc || k > 0) ? 1u : 0u);
-          mma_commit<CG>(&empty[s]);
+            for (int k = 0; k < kBK / 16; ++k)  // 16 elements of K = 32 bytes inside the swizzled row
+              mma_ss<CG>(d, ad + 2 * k, bd + 2 * k, idesc, (kb > kc || k > 0) ? 1u : 0u);
+            mma_commit<CG>(&empty[s], mask);
+            if (++s == ST) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok) mma_commit<CG>(&acc_full[b], mask);
         }
-        if (ok) mma_commit<CG>(&acc_full[b]);
       }
+      if (!ok) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
     }
-    if (!ok) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
-  } else if (warp >= 2) {  // ------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;  // a warp reaches the TMEM lanes of its number mod 4
+    __syncwarp();
+    ring_free();
+  } else {  // ------------------------------------------------------- epilogue
+    const int q = warp & 3;  // a warp reaches the TMEM lanes of its number mod 4
     const uint32_t lanes = static_cast<uint32_t>(q) << 21;  // lane 32 q in the address's upper half
-    const uint32_t t_sum = tmem + lanes + 2 * NT;
+    const int mid = (nt / CW + 1) / 2 * CW;  // columns [0, mid) and [mid, nt) for the quarter's two warps
+    const int cb = warp < 6 ? 0 : mid, ce = warp < 6 ? mid : nt;
+    const int steps = (ce - cb) / CW;
+    uint8_t* own_tile = stages + P.stg_off + (warp - 2) * P.stg;
+    const bool vec_res = P.vec_io && a.res != nullptr;
     int ai = 0;
     bool ok = true;
-    float* part = reinterpret_cast<float*>(stages);  // split: [NT][128] partial sums
     for (int tile = unit; ok && tile < P.tiles; tile += units) {
       int mb, tb;
       tile_of(tile, mb, tb);
-      const int rb = mb * CG + (CG == 2 ? static_cast<int>(rank) : 0);
-      const int64_t n = glu ? static_cast<int64_t>(rb) * 64 + q * 16 + (lane & 15)
-                            : static_cast<int64_t>(rb) * 128 + q * 32 + lane;
+      const int rb = mb * CG + side;
+      const int n0 = glu ? rb * 64 + q * 16 : rb * 128 + q * 32;  // the warp's first output feature
+      const int64_t n = n0 + (glu ? (lane & 15) : lane);
       const bool nok = n < a.N;
-      for (int kc = 0; kc < nchunk; ++kc, ++ai) {
-        const int b = ai & 1;
-        ok = mbar_wait(&acc_full[b], (ai >> 1) & 1, a.wait);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tm_fence_after();
-        const uint32_t t_acc = tmem + lanes + b * NT;
-        for (int c0 = half * (NT / 2); c0 < (half + 1) * (NT / 2); c0 += CW) {
-          uint32_t r[CW];
-          float v[CW];
-          __syncwarp();
-          tm_ld(t_acc + c0, r);
-          tm_ld_wait();
-#pragma unroll
-          for (int c = 0; c < CW; ++c) v[c] = __uint_as_float(r[c]);
-          if (kc > 0) {
-            tm_ld(t_sum + c0, r);
-            tm_ld_wait();
-#pragma unroll
-            for (int c = 0; c < CW; ++c) v[c] += __uint_as_float(r[c]);
-          }
-          if (kc < nchunk - 1) {
-#pragma unroll
-            for (int c = 0; c < CW; ++c) r[c] = __float_as_uint(v[c]);
-            tm_st(t_sum + c0, r);
-            tm_st_wait();
-          } else if (CG == 1 && P.split > 1) {
-#pragma unroll
-            for (int c = 0; c < CW; ++c) part[(c0 + c) * 128 + q * 32 + lane] = v[c];
-          } else {
-            emit<CW>(a, v, static_cast<int64_t>(tb) * NT + c0, n, nok, lane);
-          }
-        }
+      const int64_t t0 = static_cast<int64_t>(tb) * nt;
+      // steps of this warp that hold outputs (the others are past N or T)
+      int live = n0 < a.N ? steps : 0;
+      if (t0 + cb >= a.T) live = 0;
+      else if (t0 + cb + static_cast<int64_t>(live) * CW > a.T) live = static_cast<int>((a.T - t0 - cb + CW - 1) / CW);
+      uint4 rr[CW / 4] = {};
+      auto fetch_res = [&](int i) {
+        if (!vec_res || i >= live) return;
+        const int64_t t = t0 + cb + i * CW;
+        if (a.res_fmt == MOE_FMT_F32)
+          glu ? load_res<float, CW, 16>(a, rr, t, n0, lane) : load_res<float, CW, 32>(a, rr, t, n0, lane);
+        else
+          glu ? load_res<uint16_t, CW, 16>(a, rr, t, n0, lane) : load_res<uint16_t, CW, 32>(a, rr, t, n0, lane);
+      };
+      if (!SUM) fetch_res(0);  // while the tile's MMAs run (SUM: its registers hold sums until then)
+      auto arrive_empty = [&](int b) {
         tm_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (CG == 2)
-            mbar_arrive_remote(map_rank(smem_u32(&acc_empty[b]), 0));
+            mbar_arrive_remote(map_rank(smem_u32(&acc_empty[b]), rank & ~1u));
           else
             mbar_arrive(&acc_empty[b]);
         }
+      };
+      if (SUM && nchunk > 1) {
+        // sums of the chunks in registers; the last goes back into its TMEM buffer
+        float acc[NT / 32][16];
+        for (int kc = 0; kc < nchunk; ++kc) {
+          const int b = (ai + kc) & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[b], ((ai + kc) >> 1) & 1, a.wait));
+          if (!ok) break;
+          tm_fence_after();
+#pragma unroll
+          for (int g = 0; g < NT / 32; ++g) {
+            if (cb + 16 * g >= ce) break;  // warp-uniform
+            uint32_t r[16];
+            const uint32_t t = tmem + lanes + b * nt + cb + 16 * g;
+            __syncwarp();
+            tm_ld16(t, r);
+            tm_ld_wait();
+            if (kc == 0) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) acc[g][c] = __uint_as_float(r[c]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) acc[g][c] += __uint_as_float(r[c]);
+            }
+            if (kc == nchunk - 1) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) r[c] = __float_as_uint(acc[g][c]);
+              tm_st16(t, r);
+            }
+          }
+          if (kc < nchunk - 1) arrive_empty(b);
+        }
+        tm_st_wait();
+        ai += nchunk - 1;
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[ai & 1], (ai >> 1) & 1, a.wait));
       }
+      const int b = ai & 1;
+      ++ai;
+      tm_fence_after();
+      ring_free();  // once: a split cluster has one tile
+      if (!ok) break;
+      if (SUM) fetch_res(0);
+      for (int i = 0; i < steps; ++i) {
+        const int c0 = cb + i * CW;
+        if (P.split == 1 && i >= live) break;
+        uint32_t r[CW];
+        float v[CW];
+        __syncwarp();
+        if constexpr (CW == 32)
+          tm_ld32(tmem + lanes + b * nt + c0, r);
+        else
+          tm_ld16(tmem + lanes + b * nt + c0, r);
+        tm_ld_wait();
+#pragma unroll
+        for (int c = 0; c < CW; ++c) v[c] = __uint_as_float(r[c]);
+        if (P.split > 1) {
+          // to the owner of the columns: [part][column pair][128 rows] x 2 floats
+          const int own = nt / P.split;
+#pragma unroll
+          for (int c = 0; c < CW; c += 2) {
+            const int to = (c0 + c) / own, pair = (c0 + c - to * own) / 2;
+            const uint32_t dst = smem_u32(stages + P.recv_off) +
+                                 ((kpart * (own / 2) + pair) * 128 + q * 32 + lane) * 8;
+            const uint32_t peer = to * CG + side;
+            st_async_f32x2(map_rank(dst, peer), v[c], v[c + 1], map_rank(smem_u32(recv), peer));
+          }
+        } else if (P.vec_io) {
+          auto next = [&] { fetch_res(i + 1); };
+          if (glu)
+            emit_tile<CW, SUM, true>(a, v, rr, next, own_tile, t0 + c0, n0, nok, lane);
+          else
+            emit_tile<CW, SUM, false>(a, v, rr, next, own_tile, t0 + c0, n0, nok, lane);
+        } else {
+          const int64_t left = a.T - t0 - c0;
+          emit<CW>(a, v, t0 + c0, left < CW ? static_cast<int>(left) : CW, n, nok, lane);
+        }
+      }
+      arrive_empty(b);
     }
-    if (!ok && lane == 0) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
+    if (lane == 0 && !ok) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
   }
   __syncwarp();
+  tm_fence_before();
+  if (csize > 1) cluster_arrive();
 
-  if (CG == 1 && P.split > 1) {  // one tile per cluster: add the parts, a share of the columns per CTA
-    cluster_sync_all();
-    if (warp >= 2) {
-      int mb, tb;
-      tile_of(unit, mb, tb);
-      const int q = warp & 3, half = (warp - 2) >> 2;
-      const int64_t n = glu ? static_cast<int64_t>(mb) * 64 + q * 16 + (lane & 15)
-                            : static_cast<int64_t>(mb) * 128 + q * 32 + lane;
-      const int c0 = NT * static_cast<int>(rank) / P.split, c1 = NT * static_cast<int>(rank + 1) / P.split;
-      for (int c = c0 + half; c < c1; c += 2) {
-        const uint32_t off = smem_u32(stages) + (c * 128 + q * 32 + lane) * 4;
-        float v = 0.f;
-        for (int r = 0; r < P.split; ++r) v += ld_cluster_f32(map_rank(off, r));
-        const int64_t t = static_cast<int64_t>(tb) * NT + c;
-        bool nok = n < a.N && t < a.T;
-        float bias = 0.f;
-        if (a.bias && nok) bias = a.bias[(glu && lane >= 16 ? a.N : 0) + n];
-        v += bias;
-        if (glu) {
-          v = swiglu_f32(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          nok = nok && lane < 16;
-        } else {
-          v = linear_act(v, a.act);
-        }
-        if (nok) linear_store(a, t, n, v);
+  if (P.split > 1 && warp >= 2) {  // one tile per cluster: add the parts of this CTA's share of the columns
+    int mb, tb;
+    tile_of(unit, mb, tb);
+    const int q = warp & 3;
+    const int rb = mb * CG + side;
+    const int64_t n = glu ? static_cast<int64_t>(rb) * 64 + q * 16 + (lane & 15)
+                          : static_cast<int64_t>(rb) * 128 + q * 32 + lane;
+    const bool nok = n < a.N;
+    const int own = nt / P.split, pairs = own / 2;
+    const int64_t t0 = static_cast<int64_t>(tb) * nt + kpart * own;
+    const float2* got = reinterpret_cast<const float2*>(stages + P.recv_off) + q * 32 + lane;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(recv, 0, a.wait));
+    if (!ok && lane == 0) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
+    auto add = [&](int p, float& x, float& y) {
+      float2 s = got[p * 128];
+      for (int r = 1; r < P.split; ++r) {
+        const float2 g = got[(r * pairs + p) * 128];
+        s.x += g.x;
+        s.y += g.y;
       }
+      x = s.x;
+      y = s.y;
+    };
+    const int h = warp < 6 ? 0 : 1;
+    int p = h * 4;
+    for (; ok && p + 4 <= pairs; p += 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) add(p + u, v[2 * u], v[2 * u + 1]);
+      const int64_t t = t0 + 2 * p, left = a.T - t;
+      if (left > 0) emit<8>(a, v, t, left < 8 ? static_cast<int>(left) : 8, n, nok, lane);
+    }
+    for (p = pairs / 4 * 4 + h; ok && p < pairs; p += 2) {
+      float v[2];
+      add(p, v[0], v[1]);
+      const int64_t t = t0 + 2 * p, left = a.T - t;
+      if (left > 0) emit<2>(a, v, t, left < 2 ? static_cast<int>(left) : 2, n, nok, lane);
     }
   }
-  tm_fence_before();
   __syncthreads();
-  if (csize > 1) cluster_sync_all();  // no CTA leaves while another reads its shared memory or signals its barriers
+  if (csize > 1) cluster_wait();  // no CTA leaves while another sends to it or signals its barriers
   tm_fence_after();
-  if (warp == 1) tm_free_cg<CG>(tmem, kCols);
+  if (warp == 1) tm_free_cg<CG>(tmem, P.cols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -528,8 +758,13 @@ cudaError_t encode(CUtensorMap* m, const void* p, int nd, const cuuint64_t* dims
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int CG, int NT>
-cudaError_t launch(const LinearArgs& a, int split, cudaStream_t s) {
+bool io_rows(const void* p, int fmt, int64_t ld, int T) {
+  const int sz = fmt == MOE_FMT_F32 ? 4 : 2;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (T <= 1 || ld * sz % 16 == 0);
+}
+
+template <int CG, int NT, bool SUM>
+cudaError_t launch(const LinearArgs& a, int nt, int split, cudaStream_t s) {
   const bool glu = a.act == MOE_ACT_SWIGLU;
   CUtensorMap tw, tx;
   const cuuint64_t ldw = static_cast<cuuint64_t>(a.N > 1 || glu ? a.ldw : a.K) * 2;
@@ -547,34 +782,55 @@ cudaError_t launch(const LinearArgs& a, int split, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.K), static_cast<cuuint64_t>(a.T)};
-  const cuuint32_t box[2] = {kBK, NT / CG};
+  const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(nt / CG)};
   e = encode(&tx, a.x, 2, dims, &ldx, box);
   if (e != cudaSuccess) return e;
 
   TcParams P;
   P.a = a;
+  P.nt = nt;
   const int64_t rows = glu ? 2 * static_cast<int64_t>(a.N) : a.N;
   P.mblocks = static_cast<int>((rows + 128 * CG - 1) / (128 * CG));
-  P.tblocks = (a.T + NT - 1) / NT;
-  if (static_cast<int64_t>(P.mblocks) * P.tblocks * (CG == 2 ? 2 : split) >= (1LL << 31)) return cudaErrorInvalidValue;
+  P.tblocks = (a.T + nt - 1) / nt;
+  if (static_cast<int64_t>(P.mblocks) * P.tblocks * CG * split >= (1LL << 31)) return cudaErrorInvalidValue;
   P.tiles = P.mblocks * P.tblocks;
   P.kblocks = (a.K + kBK - 1) / kBK;
-  P.chunk = a.out_fmt == MOE_FMT_F32 && NT <= 128 ? kChunk : P.kblocks;
+  P.chunk = SUM ? kChunk : P.kblocks;
   P.split = split;
   P.mfast = rows <= a.T;  // the smaller operand is the one read again from L2
+  P.stage_bytes = kATile + nt / CG * kBK * 2;
+  P.cols = 32;
+  while (P.cols < static_cast<uint32_t>(2 * nt)) P.cols *= 2;
+  P.vec_io = split == 1 && io_rows(a.out, a.out_fmt, a.ldo, a.T) && (!a.res || io_rows(a.res, a.res_fmt, a.ldr, a.T));
+  constexpr int CW = (CG == 2 && !SUM) ? 32 : 16;
+  const int widest = a.out_fmt == MOE_FMT_F32 || (a.res && a.res_fmt == MOE_FMT_F32) ? 4 : 2;
+  P.stg = P.vec_io ? CW * (glu ? 16 : 32) * widest : 0;
+  const int staging = 8 * P.stg;
+  P.recv_own = split > 1 && nt * 512 <= 32768;
+  const int behind = P.recv_own ? nt * 512 : staging;
+  // a decode-sized call is small enough for two CTAs per SM, so that the next
+  // call's set-up overlaps this one's end; five stages of 18 KB on every SM
+  // still cover the DRAM latency
+  const int most_smem = NT <= 32 ? kSmemHalf : kSmemMax;
+  P.stages = (most_smem - kCtl - 1024 - behind) / P.stage_bytes;
+  if (P.stages > kMaxStages) P.stages = kMaxStages;
+  P.stg_off = P.stages * P.stage_bytes;
+  P.recv_off = P.recv_own ? P.stg_off : 0;
+  if (split > 1 && !P.recv_own && nt * 512 > P.stages * P.stage_bytes) return cudaErrorInvalidValue;
 
-  const int csize = CG == 2 ? 2 : split;
+  const int csize = CG * split;
   int units = P.tiles;
   if (split == 1) {
     const int most = matmul_ctas() / csize > 0 ? matmul_ctas() / csize : 1;
     units = units < most ? units : most;
   }
-  e = set_smem_limit(linear_tc_kernel<CG, NT>, smem_bytes<CG, NT>());
+  const int smem = kCtl + 1024 + P.stages * P.stage_bytes + behind;
+  e = set_smem_limit(linear_tc_kernel<CG, NT, SUM>, kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * csize);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<CG, NT>();
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -584,7 +840,50 @@ cudaError_t launch(const LinearArgs& a, int split, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, NT>, tw, tx, P);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, NT, SUM>, tw, tx, P);
+}
+
+struct Plan {
+  int cg, nt, split;
+};
+
+// The tile and split of least estimated time, in SM cycles.  A stage costs
+// its MMAs (2 cycles per token column) or its operands' way from L2 at about
+// 64 bytes per SM and cycle, whichever is longer; an accumulator's epilogue
+// overlaps the next tile's stages, the last one's does not; a split adds the
+// exchange of partial sums.
+Plan choose(const LinearArgs& a) {
+  const bool sum = a.out_fmt == MOE_FMT_F32;
+  const int64_t rows = a.act == MOE_ACT_SWIGLU ? 2 * static_cast<int64_t>(a.N) : a.N;
+  const int kb = (a.K + kBK - 1) / kBK;
+  const int sms = matmul_ctas();
+  Plan best{1, 16, 1};
+  double least = 1e30;
+  auto consider = [&](int cg, int nt, int split) {
+    const int64_t tiles = (rows + 128 * cg - 1) / (128 * cg) * ((a.T + nt - 1) / nt);
+    const int64_t slots = sms / (cg * split);
+    if (slots < 1 || (split > 1 && (tiles > slots || kb < 2 * split))) return;
+    const int64_t rounds = (tiles + slots - 1) / slots;
+    const double mma = 2.0 * nt, l2 = (kATile + nt / cg * 128) / 64.0;
+    const double stage = mma > l2 ? mma : l2;
+    const double main = static_cast<double>((kb + split - 1) / split) * stage;
+    const double epi = 1500.0 + 20.0 * nt;
+    double t = rounds * (main > epi ? main : epi) + 2500.0 + epi;
+    if (split > 1) t += 2000.0 + 10.0 * nt;
+    if (t < least) {
+      least = t;
+      best = Plan{cg, nt, split};
+    }
+  };
+  const int t16 = (a.T + 15) / 16 * 16;
+  for (int split = 1; split <= 8; split *= 2) {
+    for (int nt = 16; nt <= 128; nt += 16)
+      if (nt <= t16) consider(1, nt, split);
+    if (split <= 4)
+      for (int nt = 64; nt <= (sum ? 224 : 256); nt += 32)  // M = 256 takes N in steps of 32
+        if (nt < a.T + 32) consider(2, nt, split);
+  }
+  return best;
 }
 
 }  // namespace
@@ -596,22 +895,11 @@ bool linear_tc_supported(const LinearArgs& a) {
 }
 
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s) {
-  const int rows = a.act == MOE_ACT_SWIGLU ? 2 * a.N : a.N;
-  const int mb = (rows + 127) / 128, kb = (a.K + kBK - 1) / kBK;
-  const int sms = matmul_ctas();
-  // split K while the tiles leave SMs idle and every part keeps two stages or more
-  auto split_for = [&](int tiles) {
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && kb >= split * 4) split *= 2;
-    return split;
-  };
-  if (a.T <= 16) return launch<1, 16>(a, split_for(mb), s);
-  if (a.T <= 32) return launch<1, 32>(a, split_for(mb), s);
-  if (a.T <= 64) return launch<1, 64>(a, split_for(mb), s);
-  const int64_t t128 = static_cast<int64_t>(mb) * ((a.T + 127) / 128);
-  if (t128 <= sms) return launch<1, 128>(a, split_for(static_cast<int>(t128)), s);
-  if (a.out_fmt == MOE_FMT_F32) return launch<2, 128>(a, 1, s);
-  return launch<2, 256>(a, 1, s);
+  const Plan p = choose(a);
+  const bool sum = a.out_fmt == MOE_FMT_F32;
+  if (p.nt <= 32 && p.cg == 1) return sum ? launch<1, 32, true>(a, p.nt, p.split, s) : launch<1, 32, false>(a, p.nt, p.split, s);
+  if (p.cg == 1) return sum ? launch<1, 128, true>(a, p.nt, p.split, s) : launch<1, 128, false>(a, p.nt, p.split, s);
+  return sum ? launch<2, 224, true>(a, p.nt, p.split, s) : launch<2, 256, false>(a, p.nt, p.split, s);
 }
 
 }  // namespace moe
