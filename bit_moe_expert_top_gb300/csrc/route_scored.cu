@@ -11,121 +11,194 @@ namespace moe {
 
 namespace {
 
-// Two largest of a set, equal values counted as often as they occur.
-struct Top2 {
-  float a, b;
-};
-MOE_D Top2 top2_join(Top2 p, Top2 q) {
-  return p.a >= q.a ? Top2{p.a, fmaxf(p.b, q.a)} : Top2{q.a, fmaxf(q.b, p.a)};
+constexpr int kRouteWarps = 4;
+
+// Order of a value as an unsigned integer: larger value first, -0 as +0, NaN
+// (1) below -inf; 0 is left for what cannot be chosen.
+MOE_D uint32_t ord_num(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+MOE_D uint32_t ord_key(float v) { return v == v ? ord_num(v) : 1u; }
+
+// e^x, 1 / x by the hardware's approximations (2 ulp, 1 ulp).
+MOE_D float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+MOE_D float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// One warp per token; scores s and selection scores c of its experts in
-// shared memory.  Every selection is k rounds of a warp-wide maximum over
-// 64-bit keys (route_key: value, then lowest index).
-__global__ void __launch_bounds__(128) route_scored_kernel(const RouteArgs a) {
-  extern __shared__ float sm[];
+// Two largest of a set, equal values counted as often as they occur.
+MOE_D void top2_add(float& a, float& b, float v) {
+  b = fmaxf(b, fminf(a, v));
+  a = fmaxf(a, v);
+}
+
+// One warp per token, lane l holding the experts l, l + 32, ... in registers.
+// Each of the k rounds is two warp reductions in hardware (largest key, then
+// the lowest index that has it) instead of a 64-bit shuffle tree; every lane
+// keeps its two best, so a winner's lane scans its experts again only when it
+// wins a second time.  What bounds it is the issue of these instructions.
+template <int NPL>
+__global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 12 ? 12 : (NPL <= 16 ? 8 : 5))
+    route_scored_kernel(const RouteArgs a) {
+  extern __shared__ float sm[];  // groups: [warp][E] selection scores
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 4 + warp;
+  const int t = blockIdx.x * kRouteWarps + warp;
   if (t >= a.T) return;
-  float* s = sm + warp * 2 * a.E;
-  float* c = s + a.E;
   const float* row = a.logits + t * a.ldl;
-  bool nan = false;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const int per = a.E / a.n_group;
+  const bool grouped = a.n_group > 1;
+  float* c = sm + warp * a.E;
+  constexpr float kLog2e = 1.442695041f;
 
+  float l[NPL];
   float mx = -INFINITY;
-  for (int e = lane; e < a.E; e += 32) {
-    const float l = row[e];
-    s[e] = l;
-    if (l == l) mx = fmaxf(mx, l);
+  bool odd = false;  // an infinite or NaN logit
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = 32 * i + lane;
+    l[i] = e < a.E ? __ldg(row + e) : -INFINITY;
+    mx = fmaxf(mx, l[i]);  // NaN is passed over
+    odd |= e < a.E && !(fabsf(l[i]) < INFINITY);
   }
+  odd = __any_sync(0xffffffffu, odd);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float sum = 0.f;
-  for (int e = lane; e < a.E; e += 32) {
-    const float l = s[e];
-    float v;
-    if (a.score == MOE_SCORE_SIGMOID)
-      v = 1.0f / (1.0f + expf(-l));
-    else
-      v = l == mx ? 1.0f : expf(l - mx);
-    if (!(l > -INFINITY)) v = 0.f;  // masked, or NaN
-    c[e] = v;
-    sum += v;
-  }
+
+  // the unnormalised score of a logit; 0 for a masked (-inf) or NaN one
+  auto raw_score = [&](float v) {
+    float z;
+    if (softmax) {
+      z = exp2_fast((v - mx) * kLog2e);  // the difference first: v * log2(e) may overflow
+      if (odd && v == mx) z = 1.0f;
+    } else {
+      z = rcp_fast(1.0f + exp2_fast(-v * kLog2e));
+    }
+    return odd && !(v > -INFINITY) ? 0.f : z;
+  };
+  float norm = 1.0f;
+  if (softmax) {
+    float sum = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  for (int e = lane; e < a.E; e += 32) {
-    const float l = s[e];
-    float v = c[e];
-    if (a.score == MOE_SCORE_SOFTMAX && sum > 0.f) v = v / sum;
-    float cc = v + (a.bias ? a.bias[e] : 0.f);
-    if (l == -INFINITY) cc = -INFINITY;
-    if (l != l) cc = l;
-    nan |= (cc != cc);
-    s[e] = v;
-    c[e] = cc;
+    for (int i = 0; i < NPL; ++i)
+      if (32 * i + lane < a.E) sum += raw_score(l[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    norm = sum > 0.f ? 1.0f / sum : 0.f;
   }
-  __syncwarp();
+
+  uint32_t key[NPL];
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = 32 * i + lane;
+    float v = raw_score(l[i]) * norm;
+    if (a.bias && e < a.E) v += __ldg(a.bias + e);
+    if (odd) {
+      if (l[i] == -INFINITY) v = -INFINITY;
+      if (l[i] != l[i]) v = l[i];
+    }
+    nan |= e < a.E && v != v;
+    key[i] = e < a.E ? ord_key(v) : 0;
+    if (grouped && e < a.E) c[e] = v;
+  }
   if (__any_sync(0xffffffffu, nan) && lane == 0) set_err(a.dev_err, MOE_DEVERR_NAN_LOGIT);
 
-  // groups: lane g holds group g's key
-  const int per = a.E / a.n_group;
-  uint32_t kept = 0xffffffffu;
-  if (a.n_group > 1) {
-    uint64_t gkey = 0;
-    for (int g = 0; g < a.n_group; ++g) {
-      Top2 m{-INFINITY, -INFINITY};
-      for (int i = lane; i < per; i += 32) {
-        const float v = c[g * per + i];
-        if (v == v) m = top2_join(m, Top2{v, -INFINITY});
+  if (grouped) {
+    __syncwarp();
+    // lanes per group: 32 / G where that is whole (rotated starts keep the
+    // groups' lanes on different banks), else one
+    const int L = 32 % a.n_group == 0 ? 32 / a.n_group : 1;
+    const int g = lane / L, sub = lane - g * L;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < a.n_group) {
+      const int steps = (per + L - 1) / L;
+      int s = g % steps;
+      for (int i = 0; i < steps; ++i) {
+        const int j = sub + L * s;
+        if (j < per) {
+          const float v = c[g * per + j];
+          if (v == v) top2_add(m1, m2, v);
+        }
+        if (++s == steps) s = 0;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        m = top2_join(m, Top2{__shfl_xor_sync(0xffffffffu, m.a, o), __shfl_xor_sync(0xffffffffu, m.b, o)});
-      if (lane == g) gkey = route_key(a.group_top == 2 ? m.a + m.b : m.a, g);
     }
-    kept = 0;
+    for (int o = 1; o < L; o <<= 1) {
+      const float p1 = __shfl_xor_sync(0xffffffffu, m1, o), p2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      top2_add(m1, m2, p1);
+      top2_add(m1, m2, p2);
+    }
+    uint32_t gk = ord_key(a.group_top == 2 ? m1 + m2 : m1);
+    gk = __shfl_sync(0xffffffffu, gk, lane * L & 31);
+    if (lane >= a.n_group) gk = 0;
+    uint32_t kept = 0;
     for (int j = 0; j < a.topk_group; ++j) {
-      uint64_t m = gkey;
+      const uint32_t m = __reduce_max_sync(0xffffffffu, gk);
+      const unsigned who = __ballot_sync(0xffffffffu, gk == m);
+      const int w = __ffs(who) - 1;
+      kept |= 1u << w;
+      if (lane == w) gk = 0;
+    }
+    const uint32_t by = (1048576u + per - 1) / per;  // e / per = e * by >> 20 for e < 1024, per <= 512
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, m, o);
-        m = other > m ? other : m;
+    for (int i = 0; i < NPL; ++i)
+      if (!((kept >> (((32 * i + lane) * by) >> 20)) & 1)) key[i] = 0;
+  }
+
+  uint32_t best = 0, second = 0;
+  int slot = 0, slot2 = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool first = key[i] > best, next = key[i] > second;
+    slot2 = first ? slot : (next ? i : slot2);
+    second = max(second, min(best, key[i]));
+    slot = first ? i : slot;
+    best = max(best, key[i]);
+  }
+  int mine = 0;         // lane j keeps slot j
+  uint32_t taken = 0;   // this lane's experts that won
+  bool spare = true;    // (second, slot2) still stands
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t id = __reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(32 * slot + lane) : 0xffffffffu);
+    if (lane == j) mine = static_cast<int>(id);
+    if ((id & 31) == static_cast<uint32_t>(lane)) {
+      taken |= 1u << slot;
+      if (spare) {
+        best = second;
+        slot = slot2;
+        spare = false;
+      } else {
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+          if (!(taken >> i & 1) && key[i] > best) {
+            best = key[i];
+            slot = i;
+          }
       }
-      const int g = static_cast<int>(0xffffffffu - static_cast<uint32_t>(m));
-      kept |= 1u << g;
-      if (lane == g) gkey = 0;
     }
   }
 
-  uint64_t mine = 0;  // lane j keeps slot j
-  uint64_t last = ~0ull;
-  for (int j = 0; j < a.k; ++j) {
-    uint64_t m = 0;  // largest key below the last one taken
-    for (int e = lane; e < a.E; e += 32) {
-      if (!((kept >> (e / per)) & 1)) continue;
-      const uint64_t key = route_key(c[e], e);
-      if (key < last && key > m) m = key;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, m, o);
-      m = other > m ? other : m;
-    }
-    if (lane == j) mine = m;
-    last = m;
-  }
-  const int id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(mine));
-  float w = lane < a.k ? s[id] : 0.f;
+  // the bias selects, the score weighs: from the logit again (a cached load)
+  float w = lane < a.k ? raw_score(__ldg(row + mine)) * norm : 0.f;
   if (a.renorm) {
-    float tot = 0.f;
-    for (int j = 0; j < a.k; ++j) tot += __shfl_sync(0xffffffffu, w, j);
+    float tot = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
     w = tot > 0.f ? w / tot : 0.f;
   }
   if (lane < a.k) {
-    a.ids[static_cast<size_t>(t) * a.k + lane] = id;
+    a.ids[static_cast<size_t>(t) * a.k + lane] = mine;
     a.w[static_cast<size_t>(t) * a.k + lane] = w * a.scale;
   }
 }
@@ -133,8 +206,13 @@ __global__ void __launch_bounds__(128) route_scored_kernel(const RouteArgs a) {
 }  // namespace
 
 cudaError_t launch_route_scored(const RouteArgs& a, cudaStream_t s) {
-  return launch_pdl(route_scored_kernel, dim3((a.T + 3) / 4), dim3(128), static_cast<size_t>(8) * a.E * sizeof(float), s,
-                    a);
+  const dim3 grid((a.T + kRouteWarps - 1) / kRouteWarps), block(kRouteWarps * 32);
+  const size_t smem = a.n_group > 1 ? static_cast<size_t>(kRouteWarps) * a.E * sizeof(float) : 0;
+  if (a.E <= 128) return launch_pdl(route_scored_kernel<4>, grid, block, smem, s, a);
+  if (a.E <= 256) return launch_pdl(route_scored_kernel<8>, grid, block, smem, s, a);
+  if (a.E <= 384) return launch_pdl(route_scored_kernel<12>, grid, block, smem, s, a);
+  if (a.E <= 512) return launch_pdl(route_scored_kernel<16>, grid, block, smem, s, a);
+  return launch_pdl(route_scored_kernel<32>, grid, block, smem, s, a);
 }
 
 }  // namespace moe
