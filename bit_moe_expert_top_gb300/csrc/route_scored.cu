@@ -13,11 +13,11 @@ namespace {
 
 constexpr int kRouteWarps = 4;
 
-// Order of a value as an unsigned integer: larger value first, -0 as +0, NaN
+// Order of a selection score as an unsigned integer: larger value first, NaN
 // (1) below -inf; 0 is left for what cannot be chosen.
 MOE_D uint32_t ord_num(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  const uint32_t u = __float_as_uint(v);  // never -0: a score of +0 plus any bias is not
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);  // one shift, one logic operation
 }
 MOE_D uint32_t ord_key(float v) { return v == v ? ord_num(v) : 1u; }
 
@@ -43,10 +43,13 @@ MOE_D void top2_add(float& a, float& b, float v) {
 // Each of the k rounds is two warp reductions in hardware (largest key, then
 // the lowest index that has it) instead of a 64-bit shuffle tree; every lane
 // keeps its two best, so a winner's lane scans its experts again only when it
-// wins a second time.  What bounds it is the issue of these instructions.
+// wins a second time.  What bounds it is the issue of instructions: rows of
+// ordinary logits take a path without the tests for masked and NaN ones.
 template <int NPL>
 __global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 12 ? 12 : (NPL <= 16 ? 8 : 5))
     route_scored_kernel(const RouteArgs a) {
+  // slots every launch of this instance fills: NPL is the least that holds E
+  constexpr int kFull = NPL == 4 ? 0 : (NPL == 32 ? 16 : NPL - 4);
   extern __shared__ float sm[];  // groups: [warp][E] selection scores
   pdl_wait();
   pdl_trigger();
@@ -57,61 +60,93 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 12 ? 12 : (NPL <= 16 
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   const int per = a.E / a.n_group;
   const bool grouped = a.n_group > 1;
-  float* c = sm + warp * a.E;
+  float* c = sm + warp * a.E + lane;
   constexpr float kLog2e = 1.442695041f;
+  auto there = [&](int i) { return i < kFull || 32 * i + lane < a.E; };
 
   float l[NPL];
-  float mx = -INFINITY;
-  bool odd = false;  // an infinite or NaN logit
+  float mx = -INFINITY, big = 0.f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const int e = 32 * i + lane;
-    l[i] = e < a.E ? __ldg(row + e) : -INFINITY;
+    l[i] = there(i) ? __ldg(row + 32 * i + lane) : -INFINITY;
     mx = fmaxf(mx, l[i]);  // NaN is passed over
-    odd |= e < a.E && !(fabsf(l[i]) < INFINITY);
   }
-  odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (there(i)) big = fabsf(l[i]) < 1e30f ? big : 1.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  bool odd = __any_sync(0xffffffffu, big > 0.f);  // an infinite, NaN or huge logit
 
   // the unnormalised score of a logit; 0 for a masked (-inf) or NaN one
   auto raw_score = [&](float v) {
-    float z;
-    if (softmax) {
-      z = exp2_fast((v - mx) * kLog2e);  // the difference first: v * log2(e) may overflow
-      if (odd && v == mx) z = 1.0f;
-    } else {
-      z = rcp_fast(1.0f + exp2_fast(-v * kLog2e));
-    }
-    return odd && !(v > -INFINITY) ? 0.f : z;
+    if (!(v > -INFINITY)) return 0.f;
+    if (softmax) return v == mx ? 1.0f : exp2_fast((v - mx) * kLog2e);
+    return rcp_fast(1.0f + exp2_fast(-v * kLog2e));
   };
   float norm = 1.0f;
-  if (softmax) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (32 * i + lane < a.E) sum += raw_score(l[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    norm = sum > 0.f ? 1.0f / sum : 0.f;
-  }
-
   uint32_t key[NPL];
-  bool nan = false;
+  if (!odd) {
+    bool nan = false;
+    float z[NPL];
+    if (softmax) {
+      const float shift = -mx * kLog2e;
+      float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = 32 * i + lane;
-    float v = raw_score(l[i]) * norm;
-    if (a.bias && e < a.E) v += __ldg(a.bias + e);
-    if (odd) {
+      for (int i = 0; i < NPL; ++i) {
+        z[i] = exp2_fast(fmaf(l[i], kLog2e, shift));
+        sum += z[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      norm = 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) z[i] *= norm;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) z[i] = rcp_fast(1.0f + exp2_fast(-l[i] * kLog2e));
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (there(i)) z[i] += __ldg(a.bias + 32 * i + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      nan |= z[i] != z[i];
+      key[i] = there(i) ? ord_num(z[i]) : 0;
+    }
+    if (grouped) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (there(i)) c[32 * i] = z[i];
+    }
+    odd = __any_sync(0xffffffffu, nan);  // from the bias
+  }
+  if (odd) {
+    norm = 1.0f;
+    if (softmax) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (there(i)) sum += raw_score(l[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      norm = sum > 0.f ? 1.0f / sum : 0.f;
+    }
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      float v = raw_score(l[i]) * norm;
+      if (a.bias && there(i)) v += __ldg(a.bias + 32 * i + lane);
       if (l[i] == -INFINITY) v = -INFINITY;
       if (l[i] != l[i]) v = l[i];
+      nan |= there(i) && v != v;
+      key[i] = there(i) ? ord_key(v) : 0;
+      if (grouped && there(i)) c[32 * i] = v;
     }
-    nan |= e < a.E && v != v;
-    key[i] = e < a.E ? ord_key(v) : 0;
-    if (grouped && e < a.E) c[e] = v;
+    if (__any_sync(0xffffffffu, nan) && lane == 0) set_err(a.dev_err, MOE_DEVERR_NAN_LOGIT);
   }
-  if (__any_sync(0xffffffffu, nan) && lane == 0) set_err(a.dev_err, MOE_DEVERR_NAN_LOGIT);
 
   if (grouped) {
     __syncwarp();
@@ -126,7 +161,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 12 ? 12 : (NPL <= 16 
       for (int i = 0; i < steps; ++i) {
         const int j = sub + L * s;
         if (j < per) {
-          const float v = c[g * per + j];
+          const float v = sm[warp * a.E + g * per + j];
           if (v == v) top2_add(m1, m2, v);
         }
         if (++s == steps) s = 0;
