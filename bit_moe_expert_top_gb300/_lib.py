@@ -304,9 +304,10 @@ def _rows(who, t, T: int, cols: int) -> int:
     """Row stride of a [T, cols] tensor whose rows are contiguous (0: no tensor)."""
     if t is None:
         return 0
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        _refuse(who, f"shape {tuple(t.shape)} / strides {t.stride()}, wanted contiguous rows [{T}, {cols}]")
-    return t.stride(0) if T > 1 else cols
+    s = t.stride()
+    if t.shape != (T, cols) or (s[1] != 1 and cols > 1):
+        _refuse(who, f"shape {tuple(t.shape)} / strides {s}, wanted contiguous rows [{T}, {cols}]")
+    return s[0] if T > 1 else cols
 
 
 def _flat(who, t, n: int):

@@ -243,33 +243,40 @@ MOE_D float gelu_tc(float v) {
   return v < 0.f ? h : v - h;
 }
 
+// This lane's bias: of its output feature, SwiGLU: of its gate and up rows.
+struct Bias {
+  float b, u;
+};
+MOE_D Bias load_bias(const LinearArgs& a, int64_t n, bool nok) {
+  Bias r{0.f, 0.f};
+  if (a.bias && nok) {
+    r.b = __ldg(a.bias + n);
+    if (a.act == MOE_ACT_SWIGLU) r.u = __ldg(a.bias + a.N + n);
+  }
+  return r;
+}
+
 // Bias and activation of this lane's CW columns.  Without SwiGLU output j of
 // the lane is column j; with it lanes 0-15 hold gate rows and lanes 16-31 the
 // up rows of the same outputs: of columns (2j, 2j + 1) the low half finishes
 // the first and the high half the second, so output j is column 2j + lane/16.
-// n: the lane's output feature (nok: inside N).
 template <int CW, bool GLU>
-MOE_D void activate(const LinearArgs& a, float (&v)[CW], float (&o)[GLU ? CW / 2 : CW], int64_t n, bool nok, int lane) {
+MOE_D void activate(int act, const Bias& bias, const float (&v)[CW], float (&o)[GLU ? CW / 2 : CW], int lane) {
   if constexpr (GLU) {
     const bool hi = lane >= 16;
-    float bg = 0.f, bu = 0.f;
-    if (a.bias && nok) {
-      bg = __ldg(a.bias + n);
-      bu = __ldg(a.bias + a.N + n);
-    }
 #pragma unroll
     for (int c = 0; c < CW / 2; ++c) {
       const float other = __shfl_xor_sync(0xffffffffu, hi ? v[2 * c] : v[2 * c + 1], 16);
-      o[c] = silu_tc((hi ? other : v[2 * c]) + bg) * ((hi ? v[2 * c + 1] : other) + bu);
+      o[c] = silu_tc((hi ? other : v[2 * c]) + bias.b) * ((hi ? v[2 * c + 1] : other) + bias.u);
     }
   } else {
-    const float b = (a.bias && nok) ? __ldg(a.bias + n) : 0.f;
 #pragma unroll
-    for (int c = 0; c < CW; ++c) o[c] = v[c] + b;
-    if (a.act == MOE_ACT_SILU) {
+    for (int c = 0; c < CW; ++c) o[c] = v[c] + bias.b;
+    if (act == MOE_ACT_NONE) return;
+    if (act == MOE_ACT_SILU) {
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[c] = silu_tc(o[c]);
-    } else if (a.act == MOE_ACT_GELU) {
+    } else {
 #pragma unroll
       for (int c = 0; c < CW; ++c) o[c] = gelu_tc(o[c]);
     }
@@ -329,55 +336,55 @@ template <int CW>
 MOE_D void emit(const LinearArgs& a, float (&v)[CW], int64_t t0, int nc, int64_t n, bool nok, int lane) {
   if (a.act == MOE_ACT_SWIGLU) {
     float o[CW / 2];
-    activate<CW, true>(a, v, o, n, nok, lane);
+    activate<CW, true>(a.act, load_bias(a, n, nok), v, o, lane);
     const int hi = lane >> 4, cnt = (nc - hi + 1) / 2;
     if (nok && cnt > 0) emit_rows<CW / 2>(a, o, t0 + hi, 2, cnt, n);
   } else {
     float o[CW];
-    activate<CW, false>(a, v, o, n, nok, lane);
+    activate<CW, false>(a.act, load_bias(a, n, nok), v, o, lane);
     if (nok) emit_rows<CW>(a, o, t0, 1, nc, n);
   }
 }
 
 // A warp's tile [CW tokens][W features] of out or res moves in 16-byte pieces,
-// lane l taking pieces l, l + 32, ...; f is called with the piece's number,
-// the address of its first element and how many of its elements lie inside N
-// (0: none, or the token is past T).
-template <typename E, int CW, int W, typename P, typename F>
-MOE_D void for_pieces(const LinearArgs& a, P* base, int64_t ld, int64_t t0, int n0, int lane, F&& f) {
-  constexpr int kPer = 16 / sizeof(E);   // elements of a piece
-  constexpr int kRow = W / kPer;         // pieces of a row
-  constexpr int kPieces = CW * kRow;
-#pragma unroll
-  for (int i = 0; i < (kPieces + 31) / 32; ++i) {
-    const int p = lane + 32 * i;
-    const int64_t t = t0 + p / kRow;
-    const int n = n0 + p % kRow * kPer;
-    int in = t < a.T && p < kPieces ? a.N - n : 0;
-    in = in < 0 ? 0 : (in > kPer ? kPer : in);
-    f(i, p, base + t * ld + n, in);
-  }
-}
+// lane l taking pieces l, l + 32, ...  Its pieces start `first` elements into
+// the tile's rows and lie kStep rows apart.
+template <typename E, int CW, int W>
+struct Pieces {
+  static constexpr int kPer = 16 / sizeof(E);  // elements of a piece
+  static constexpr int kRow = W / kPer;        // pieces of a row
+  static constexpr int kStep = 32 / kRow;      // rows between a lane's pieces
+  static constexpr int kCount = CW / kStep > 0 ? CW / kStep : 1;
+  static MOE_D int row(int lane) { return lane / kRow; }
+  static MOE_D int col(int lane) { return lane % kRow * kPer; }
+};
 
 // The residual of one step into registers (issued a step ahead of its use).
+// t0, n0: the tile's first token and feature.
 template <typename E, int CW, int W>
 MOE_D void load_res(const LinearArgs& a, uint4 (&r)[CW / 4], int64_t t0, int n0, int lane) {
-  for_pieces<E, CW, W>(a, static_cast<const E*>(a.res), a.ldr, t0, n0, lane, [&](int i, int, const E* src, int in) {
-    if (in == 16 / sizeof(E)) {
-      r[i] = *reinterpret_cast<const uint4*>(src);
-    } else if (in > 0) {
-      E e[16 / sizeof(E)];
+  using Q = Pieces<E, CW, W>;
+  const int n = n0 + Q::col(lane);
+  const int64_t t = t0 + Q::row(lane);
+  const E* src = static_cast<const E*>(a.res) + t * a.ldr + n;
+  if (t0 + CW <= a.T && n0 + W <= a.N) {
 #pragma unroll
-      for (int k = 0; k < 16 / static_cast<int>(sizeof(E)); ++k) e[k] = k < in ? src[k] : E(0);
-      r[i] = *reinterpret_cast<const uint4*>(e);
-    }
-  });
+    for (int i = 0; i < Q::kCount; ++i) r[i] = *reinterpret_cast<const uint4*>(src + i * Q::kStep * a.ldr);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < Q::kCount; ++i) {
+    E e[Q::kPer];
+#pragma unroll
+    for (int k = 0; k < Q::kPer; ++k)
+      e[k] = t + i * Q::kStep < a.T && n + k < a.N ? src[i * Q::kStep * a.ldr + k] : E(0);
+    r[i] = *reinterpret_cast<const uint4*>(e);
+  }
 }
 template <typename E, int CW, int W, int M>
 MOE_D void add_res(const uint4 (&rr)[CW / 4], uint8_t* tile, float (&o)[M], int lane) {
-  constexpr int kPieces = CW * W * static_cast<int>(sizeof(E)) / 16;
 #pragma unroll
-  for (int i = 0; i < (kPieces + 31) / 32; ++i) reinterpret_cast<uint4*>(tile)[lane + 32 * i] = rr[i];
+  for (int i = 0; i < Pieces<E, CW, W>::kCount; ++i) reinterpret_cast<uint4*>(tile)[lane + 32 * i] = rr[i];
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < M; ++c) o[c] += widen(reinterpret_cast<const E*>(tile)[32 * c + lane]);
@@ -388,12 +395,13 @@ MOE_D void add_res(const uint4 (&rr)[CW / 4], uint8_t* tile, float (&o)[M], int 
 // lane sits at 32 c + lane of the tile (SwiGLU: (2c + lane/16) * 16 + lane%16,
 // the same).
 template <int CW, bool F32, bool GLU, typename N>
-MOE_D void emit_tile(const LinearArgs& a, float (&v)[CW], const uint4 (&rr)[CW / 4], N&& next, uint8_t* tile, int64_t t0,
-                     int n0, bool nok, int lane) {
+MOE_D void emit_tile(const LinearArgs& a, const Bias& bias, const float (&v)[CW], const uint4 (&rr)[CW / 4], N&& next,
+                     uint8_t* tile, int64_t t0, int n0, int lane) {
   constexpr int W = GLU ? 16 : 32, M = GLU ? CW / 2 : CW;
   using E = typename Elem<F32 ? 4 : 2>::type;
+  using Q = Pieces<E, CW, W>;
   float o[M];
-  activate<CW, GLU>(a, v, o, n0 + lane % W, nok, lane);
+  activate<CW, GLU>(a.act, bias, v, o, lane);
   if (a.res) {
     if (a.res_fmt == MOE_FMT_F32)
       add_res<float, CW, W>(rr, tile, o, lane);
@@ -409,13 +417,22 @@ MOE_D void emit_tile(const LinearArgs& a, float (&v)[CW], const uint4 (&rr)[CW /
     reinterpret_cast<E*>(tile)[32 * c + lane] = e;
   }
   __syncwarp();
-  for_pieces<E, CW, W>(a, static_cast<E*>(a.out), a.ldo, t0, n0, lane, [&](int, int p, E* dst, int in) {
-    if (in == 16 / sizeof(E)) {
-      *reinterpret_cast<uint4*>(dst) = reinterpret_cast<const uint4*>(tile)[p];
-    } else if (in > 0) {
-      for (int k = 0; k < in; ++k) dst[k] = reinterpret_cast<const E*>(tile)[p * (16 / sizeof(E)) + k];
-    }
-  });
+  const int n = n0 + Q::col(lane);
+  const int64_t t = t0 + Q::row(lane);
+  E* dst = static_cast<E*>(a.out) + t * a.ldo + n;
+  if (t0 + CW <= a.T && n0 + W <= a.N) {
+    uint4 w[Q::kCount];
+#pragma unroll
+    for (int i = 0; i < Q::kCount; ++i) w[i] = reinterpret_cast<const uint4*>(tile)[lane + 32 * i];
+#pragma unroll
+    for (int i = 0; i < Q::kCount; ++i) *reinterpret_cast<uint4*>(dst + i * Q::kStep * a.ldo) = w[i];
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < Q::kCount; ++i)
+      if (t + i * Q::kStep < a.T)
+        for (int k = 0; k < Q::kPer && n + k < a.N; ++k)
+          dst[i * Q::kStep * a.ldo + k] = reinterpret_cast<const E*>(tile)[(lane + 32 * i) * Q::kPer + k];
+  }
   __syncwarp();
 }
 
@@ -654,9 +671,11 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
       ring_free();  // once: a split cluster has one tile
       if (!ok) break;
       if (SUM) fetch_res(0);
-      for (int i = 0; i < steps; ++i) {
+      const Bias bias = load_bias(a, n, nok);
+      const int todo = P.split == 1 ? live : steps;
+#pragma unroll 1
+      for (int i = 0; i < todo; ++i) {
         const int c0 = cb + i * CW;
-        if (P.split == 1 && i >= live) break;
         uint32_t r[CW];
         float v[CW];
         __syncwarp();
@@ -681,9 +700,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
         } else if (P.vec_io) {
           auto next = [&] { fetch_res(i + 1); };
           if (glu)
-            emit_tile<CW, SUM, true>(a, v, rr, next, own_tile, t0 + c0, n0, nok, lane);
+            emit_tile<CW, SUM, true>(a, bias, v, rr, next, own_tile, t0 + c0, n0, lane);
           else
-            emit_tile<CW, SUM, false>(a, v, rr, next, own_tile, t0 + c0, n0, nok, lane);
+            emit_tile<CW, SUM, false>(a, bias, v, rr, next, own_tile, t0 + c0, n0, lane);
         } else {
           const int64_t left = a.T - t0 - c0;
           emit<CW>(a, v, t0 + c0, left < CW ? static_cast<int>(left) : CW, n, nok, lane);
