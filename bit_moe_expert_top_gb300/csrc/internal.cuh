@@ -208,6 +208,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 // on the tensor cores (linear_tc.cu): K, strides and addresses that TMA takes
 bool linear_tc_supported(const LinearArgs& a);
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s);
+// T <= kFewTokens, same conditions (linear_few.cu)
+constexpr int kFewTokens = 16;
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 
 // ---- diagnostics (diag.cu)
 // One warp waits with the pipelines' bounded wait, limit `cycles`, on a

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) linear_kernel(const LinearArgs a) {
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  if (linear_tc_supported(a)) return launch_linear_tc(a, s);
+  if (linear_tc_supported(a)) return a.T <= kFewTokens ? launch_linear_few(a, s) : launch_linear_tc(a, s);
   const int gt = (a.T + kLT - 1) / kLT;
   const dim3 grid((a.N + kLT - 1) / kLT, gt < 65535 ? gt : 65535);
   if (a.act == MOE_ACT_SWIGLU) return launch_pdl(linear_kernel<true>, grid, dim3(256), 0, s, a);

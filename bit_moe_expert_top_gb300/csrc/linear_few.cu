@@ -1,0 +1,163 @@
+// Dense matrix product for a few tokens (T <= 16): the weights stream once from
+// DRAM straight into the fragments of warp-level matrix instructions.
+//
+// A warp multiplies 16 tokens (A, zero rows past T) by 8 weight rows (B) per
+// mma.sync m16n8k16.  A sum over K may take K in any order, so lane l takes
+// 16 contiguous bytes of K (8 elements at 8 (l mod 4) of a block of 32) of
+// weight row l/4 and of token rows l/4 and l/4 + 8: two instructions' worth of
+// both operands, with no shared memory on the way.  The blocks of 32 are dealt
+// round-robin to the CTA's warps, F weight-row groups per warp share each
+// token fragment, and the warps' partial sums meet in shared memory and are
+// added in warp order.
+//
+// Bound by DRAM: 8 tokens x 4096 gate and up rows x 4096 take 7.3 us (4600
+// GB/s, 2.3 us over the copy rate's time).  On tcgen05 the same call pays for
+// TMEM, the ring's first fill and an exchange over the cluster: 9.4 us, and
+// 6.0 against 2.9 us for 384 rows.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.cuh"
+#include "linear_common.cuh"
+
+namespace moe {
+
+namespace {
+
+MOE_D uint4 ld_stream(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+MOE_D uint4 ld_now(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+MOE_D void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// R output groups of 8 per CTA (SwiGLU: with their up rows, F = 2R row
+// groups) and W warps, two CTAs of 16 or four of 8 per SM; TA = 1: T <= 8, 2:
+// T <= 16; U blocks of K in flight per warp.
+template <int R, bool GLU, int TA, int W>
+__global__ void __launch_bounds__(W * 32, 32 / W) linear_few_kernel(const LinearArgs a) {
+  constexpr int F = GLU ? 2 * R : R, U = 4;
+  __shared__ float part[W][F][32 * 4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n0 = blockIdx.x * 8 * R;
+  const int kl = 8 * (lane & 3) < a.K ? 8 * (lane & 3) : 0;  // K < 32: lanes past it read the first piece
+  const bool kany = 8 * (lane & 3) < a.K;
+  const uint16_t* wrow[F];
+  bool wok[F];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int n = n0 + (GLU ? f / 2 : f) * 8 + (lane >> 2);
+    wok[f] = n < a.N;
+    wrow[f] = a.w + (wok[f] ? static_cast<int64_t>(GLU && (f & 1) ? a.N : 0) + n : 0) * a.ldw + kl;
+  }
+  const uint16_t* xrow[TA];
+  bool xok[TA];
+#pragma unroll
+  for (int i = 0; i < TA; ++i) {
+    const int t = (lane >> 2) + 8 * i;
+    xok[i] = t < a.T;
+    xrow[i] = a.x + (xok[i] ? t : 0) * a.ldx + kl;
+  }
+  const int nb = (a.K + 31) / 32;
+  // With few rows (one group per CTA) there is little to stream and latency
+  // counts: the rows go to L2 at once, before the wait for the preceding
+  // kernel (a prefetch reads no value).  2.9 against 3.35 us for 8 x 384 x
+  // 4096; with more rows it only disturbs the loads' order (24 -> 28 us for
+  // 16384 rows).
+  if (F == 1 && tid < 8 && n0 + tid < a.N) prefetch_l2(a.w + (n0 + tid) * a.ldw, static_cast<uint32_t>(a.K) * 2);
+  pdl_wait();
+  pdl_trigger();
+
+  float d[F][4] = {};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int b0 = warp; b0 < nb; b0 += W * U) {
+    uint4 w[U][F], x[U][TA];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (b0 + u * W) * 32;
+      // K is a multiple of 8: a piece is inside or past the end.  Every load
+      // is issued (past the end: the row's first piece, replaced by zeros
+      // below); under a condition each would wait for its branch
+      const int kk = k + kl < a.K ? k : 0;
+#pragma unroll
+      for (int f = 0; f < F; ++f) w[u][f] = ld_stream(wrow[f] + kk);
+#pragma unroll
+      for (int i = 0; i < TA; ++i) x[u][i] = ld_now(xrow[i] + kk);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool kin = kany && (b0 + u * W) * 32 + kl < a.K;
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        if (!kin || !wok[f]) w[u][f] = zero;
+#pragma unroll
+      for (int i = 0; i < TA; ++i)
+        if (!kin || !xok[i]) x[u][i] = zero;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint4 lo = x[u][0], hi = TA == 2 ? x[u][TA - 1] : zero;
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        mma_bf16(d[f], lo.x, hi.x, lo.y, hi.y, w[u][f].x, w[u][f].y);
+        mma_bf16(d[f], lo.z, hi.z, lo.w, hi.w, w[u][f].z, w[u][f].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < F; ++f) *reinterpret_cast<float4*>(&part[warp][f][lane * 4]) = make_float4(d[f][0], d[f][1], d[f][2], d[f][3]);
+  __syncthreads();
+  // output j of the CTA: token j / (8R), feature j % (8R)
+  for (int j = tid; j < TA * 8 * 8 * R; j += W * 32) {
+    const int t = j / (8 * R), i = j % (8 * R), n = n0 + i;
+    if (t >= a.T || n >= a.N) continue;
+    // fragment: token t at lane 4 (t mod 8) + (i mod 8) / 2, element 2 (t / 8) + i mod 2
+    const int e = (4 * (t & 7) + (i & 7) / 2) * 4 + 2 * (t >> 3) + (i & 1), f = GLU ? 2 * (i / 8) : i / 8;
+    float v = 0.f, u = 0.f;
+#pragma unroll
+    for (int s = 0; s < W; ++s) {
+      v += part[s][f][e];
+      if (GLU) u += part[s][f + (GLU ? 1 : 0)][e];
+    }
+    if (a.bias) {
+      v += a.bias[n];
+      if (GLU) u += a.bias[a.N + n];
+    }
+    linear_store(a, t, n, GLU ? swiglu_f32(v, u) : linear_act(v, a.act));
+  }
+}
+
+template <int R, bool GLU, int W>
+cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
+  const dim3 grid((a.N + 8 * R - 1) / (8 * R)), block(W * 32);
+  if (a.T <= 8) return launch_pdl(linear_few_kernel<R, GLU, 1, W>, grid, block, 0, s, a);
+  return launch_pdl(linear_few_kernel<R, GLU, 2, W>, grid, block, 0, s, a);
+}
+
+}  // namespace
+
+// 16 warps per CTA share its K while all CTAs run at once (two per SM), else 8
+// (8 tokens: 4096 gate and up rows x 4096 7.3 us against 8.8; 7168 rows x 2048
+// 7.0 against 6.4, 16384 rows x 4096 24.4 against 22.4).
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s) {
+  const int groups = (a.N + 7) / 8, sms = device_info().sms;
+  if (a.act == MOE_ACT_SWIGLU) return groups <= 2 * sms ? launch<1, true, 16>(a, s) : launch<1, true, 8>(a, s);
+  if (groups < sms + sms / 2) return launch<1, false, 16>(a, s);
+  return groups <= 4 * sms ? launch<2, false, 16>(a, s) : launch<2, false, 8>(a, s);
+}
+
+}  // namespace moe
