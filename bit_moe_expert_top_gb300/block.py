@@ -1,0 +1,118 @@
+"""One MoE block around a routed-expert layer, driven through libmoe's C ABI.
+
+``MoEBlock`` chains, on one stream,
+
+    moe_add_rmsnorm -> moe_linear (router) -> moe_route_scored
+        -> the layer's experts (MoELayer.experts) -> shared expert (moe_linear, twice)
+
+from the residual stream to the block's output.  The residual is updated in
+place (r <- r + x, x being the output of what came before, e.g. attention), the
+router and the experts read its norm, and the block's output is what the next
+norm adds to r.  Layers whose experts read MXFP8 rows get them from the norm
+itself, gathered without a second quantisation.
+
+No arithmetic happens here: every step runs in the library's kernels.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _lib as L
+from .layer import MoELayer, StepBuffers
+
+
+@dataclass
+class BlockBuffers:
+    step: StepBuffers
+    normed: torch.Tensor               # bf16 [T, H]
+    q: Optional[torch.Tensor]          # the same rows as MXFP8 codes and scales
+    q_scale: Optional[torch.Tensor]
+    logits: torch.Tensor               # float32 [T, E]
+    h: Optional[torch.Tensor]          # shared expert, bf16 [T, shared I]
+
+
+class MoEBlock:
+    def __init__(self, layer: MoELayer, gain: torch.Tensor, router: torch.Tensor, *, shared=None,
+                 balance: Optional[torch.Tensor] = None, router_bias: Optional[torch.Tensor] = None,
+                 score: int = L.SCORE_SOFTMAX, n_group: int = 1, topk_group: int = 1, group_top: int = 1,
+                 renorm: bool = True, scale: float = 1.0, eps: float = 1e-6):
+        """Device tensors: gain [H] (float32 or bf16); router [E, H] bf16 with
+        router_bias float32 [E]; shared = (w1 [2 I', H], w2 [H, I']) bf16, gate
+        rows first, or None; balance float32 [E]: the bias that selects but
+        does not weigh (moe_route_scored, whose arguments the rest are)."""
+        E, H = layer.E, layer.H
+        if tuple(router.shape) != (E, H) or gain.numel() != H:
+            raise ValueError(f"router {tuple(router.shape)} / gain {tuple(gain.shape)}: wanted [{E}, {H}] and [{H}]")
+        if shared is not None and (shared[0].shape[1] != H or shared[1].shape[0] != H
+                                   or shared[0].shape[0] != 2 * shared[1].shape[1]):
+            raise ValueError("shared expert: w1 [2 I', H], w2 [H, I']")
+        self.layer, self.gain, self.router, self.router_bias = layer, gain, router, router_bias
+        self.shared, self.eps = shared, eps
+        self.routing = dict(bias=balance, score=score, n_group=n_group, topk_group=topk_group, group_top=group_top,
+                            renorm=renorm, scale=scale)
+
+    def buffers(self, T: int) -> BlockBuffers:
+        ly = self.layer
+        dev, H = ly.device, ly.H
+        mx = ly.reads_mxfp8()
+        return BlockBuffers(
+            step=ly.buffers(T),
+            normed=torch.empty((T, H), dtype=torch.bfloat16, device=dev),
+            q=torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None,
+            q_scale=torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if mx else None,
+            logits=torch.empty((T, ly.E), dtype=torch.float32, device=dev),
+            h=(torch.empty((T, self.shared[1].shape[1]), dtype=torch.bfloat16, device=dev)
+               if self.shared is not None else None),
+        )
+
+    def step(self, x: torch.Tensor, residual: torch.Tensor, b: BlockBuffers) -> torch.Tensor:
+        """x [T, H] bf16 or float32, residual [T, H] float32 or bf16 (updated in
+        place); returns the block's output [T, H] in the layer's out_fmt (a
+        buffer of b, overwritten by the next step)."""
+        ly, s = self.layer, b.step
+        L.moe_add_rmsnorm(x, self.gain, self.eps, res=residual, sum_out=residual, out=b.normed, q=b.q,
+                          q_scale=b.q_scale)
+        L.moe_linear(b.normed, self.router, b.logits, bias=self.router_bias, dev_err=s.dev_err)
+        L.moe_route_scored(b.logits, ly.k, s.ids, s.w, dev_err=s.dev_err, **self.routing)
+        out = ly.experts(b.normed, s, x_mx=None if b.q is None else (b.q, b.q_scale))
+        if self.shared is not None:
+            w1, w2 = self.shared
+            L.moe_linear(b.normed, w1, b.h, act=L.ACT_SWIGLU, dev_err=s.dev_err)
+            L.moe_linear(b.h, w2, out, res=out, dev_err=s.dev_err)  # onto the routed experts' output
+        return out
+
+    def capture(self, T: int, res_dtype: torch.dtype = torch.float32) -> "BlockGraph":
+        """The whole step for T tokens captured once into a CUDA graph."""
+        return BlockGraph(self, T, res_dtype)
+
+
+class BlockGraph:
+    """A captured block step: ``run(x, residual)`` copies both into the graph's
+    own buffers and replays; ``out`` is the block's output and ``residual`` the
+    updated residual (both overwritten by every run)."""
+
+    def __init__(self, block: MoEBlock, T: int, res_dtype: torch.dtype):
+        dev, H = block.layer.device, block.layer.H
+        self.block = block
+        self.x = torch.zeros((T, H), dtype=torch.bfloat16, device=dev)
+        self.residual = torch.zeros((T, H), dtype=res_dtype, device=dev)
+        self.bufs = block.buffers(T)
+        s = torch.cuda.Stream(device=dev)
+        s.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(s):  # warm once outside the capture (library set-up, smem limits)
+            block.step(self.x, self.residual, self.bufs)
+        torch.cuda.current_stream(dev).wait_stream(s)
+        torch.cuda.synchronize(dev)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.out = block.step(self.x, self.residual, self.bufs)
+        torch.cuda.synchronize(dev)
+
+    def run(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        self.x.copy_(x, non_blocking=True)
+        self.residual.copy_(residual, non_blocking=True)
+        self.graph.replay()
+        return self.out

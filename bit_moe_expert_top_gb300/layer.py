@@ -269,14 +269,31 @@ class MoELayer:
                                       dev_err=b.dev_err)
             return b.out
         L.moe_route(logits, k, b.ids, b.w, b.dev_err)
+        return self.experts(x, b, ev=ev)
+
+    def reads_mxfp8(self) -> bool:
+        """Whether the experts' matmuls read the token rows as MXFP8 only."""
+        return self.fmt in ("fp8", "mxfp4")
+
+    def experts(self, x: Optional[torch.Tensor], b: StepBuffers, x_mx=None, ev: Optional[list] = None) -> torch.Tensor:
+        """The step after routing: grouping, expert matmuls and combine for the
+        ids and weights in b.ids / b.w, whoever routed (moe_route,
+        moe_route_scored).  x as step's; x_mx = (codes, scales): the token rows
+        as MXFP8 already (moe_add_rmsnorm), gathered as they are instead of
+        being quantised from x (layers whose reads_mxfp8())."""
+        T = b.ids.shape[0]
+        self._ev = ev
+        E, H, I, k = self.E, self.H, self.I, self.k
+        if self.reads_mxfp8():
+            if x_mx is not None:
+                self._permute(b, dev_err=b.dev_err)
+                L.moe_gather_mxfp8(x_mx[0], x_mx[1], b.inv, k, b.x_perm, b.x_perm_scale)
+            else:
+                self._permute(b, x=x, act_fmt=L.FMT_MXFP8, x_perm=b.x_perm, x_perm_scale=b.x_perm_scale,
+                              dev_err=b.dev_err)
         if self.fmt == "fp8":
-            tc = self.use_gemm(T)
-            self._permute(b, x=x, act_fmt=L.FMT_MXFP8, x_perm=b.x_perm,
-                          x_perm_scale=b.x_perm_scale, dev_err=b.dev_err)
-            self._fp8_experts(b, tc)
+            self._fp8_experts(b, self.use_gemm(T))
         elif self.fmt == "mxfp4":
-            self._permute(b, x=x, act_fmt=L.FMT_MXFP8, x_perm=b.x_perm,
-                          x_perm_scale=b.x_perm_scale, dev_err=b.dev_err)
             with self._timed("mx4_fc1_gemm"):
                 L.moe_mxfp4_mm(L.STAGE_FC1_SWIGLU, b.x_perm, L.FMT_MXFP8, b.offsets, E, I, H, b.h, L.FMT_MXFP8,
                                e2m1=self.q1, e8m0=self.e1, act_scale=b.x_perm_scale, out_scale=b.h_scale,
