@@ -66,16 +66,40 @@ MOE_D void store8(void* p, int fmt, int64_t i, const float (&f)[8]) {
   }
 }
 
+// A sum carried as h + l (h the rounded sum, l what its roundings lost).
+struct Sum2 {
+  float h, l;
+};
+MOE_D Sum2 add2(Sum2 a, Sum2 b) {
+  const float s = a.h + b.h, t = s - a.h;
+  return Sum2{s, (a.h - (s - t)) + (b.h - t) + (a.l + b.l)};
+}
+
+// n = y * inv * g (inv = ih + il), rounded to odd: the fp32 value next to the
+// exact product whose last bit is set, from which a rounding to bf16 is that
+// of the exact product.
+MOE_D float norm_odd(float y, float ih, float il, float g) {
+  const float t = y * ih, te = fmaf(y, il, fmaf(y, ih, -t));
+  const float p = t * g, pe = fmaf(te, g, fmaf(t, g, -p));
+  const float n = p + pe, r = (p - n) + pe;
+  const uint32_t u = __float_as_uint(n);
+  if (r == 0.f || (u & 1) || !(fabsf(n) < INFINITY)) return n;
+  return __uint_as_float((r > 0.f) == (n > 0.f) ? u + 1 : u - 1);
+}
+// Whether the largest element of a block is a few fp32 steps from the point
+// where its bf16 rounding becomes the next power of two.
+MOE_D bool near_power(float amax) { return (__float_as_uint(amax) & 0x7fffffu) - 0x7f7ff8u <= 16u; }
+
 // One CTA per row (rows of one warp: eight a CTA), the whole row in registers:
 // thread i of the row holds the 8-element pieces i, i + threads, ... (V of
-// them), so x and res are read once: bound by DRAM, 152 us at 16373 x 7168 with
-// bf16 residual and MXFP8 output (6960 GB/s, 1.03 of the copy rate).  Four
+// them), so x and res are read once: bound by DRAM, 155 us at 16373 x 7168 with
+// bf16 residual and MXFP8 output (6850 GB/s, 1.01 of the copy rate).  Four
 // lanes hold one MXFP8 block.  WIDE: 16-byte accesses, formats X32 / RES (0
 // none, 1 bf16, 2 fp32); else element by element, formats read from the
 // arguments.  Both sum in the same order, and V depends on H alone: a row's
 // bits depend neither on alignment nor on T.
 template <int V, bool WIDE, bool X32, int RES>
-__global__ void __launch_bounds__(V == 2 ? 256 : 512) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[32];
   pdl_wait();
   pdl_trigger();
@@ -134,16 +158,24 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 512) add_rmsnorm_kernel(const N
     for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
   }
   if (!a.out && !a.q) return;
+  // sum over the lanes and warps, inv = ih + il = 1 / sqrt(mean + eps): the
+  // bits that the last and largest steps lose are kept (the sum is then 1.5e-8
+  // off on average, 3.8e-8 without), for blocks whose scale hangs on them
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  Sum2 tot{ss, 0.f};
   if (nth > 32) {
     if (lane == 0) part[tid >> 5] = ss;
     __syncthreads();
-    ss = lane < (nth >> 5) ? part[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    tot = Sum2{part[0], 0.f};
+    for (int w = 1; w < nth >> 5; ++w) tot = add2(tot, Sum2{part[w], 0.f});
   }
-  const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+  const float h = static_cast<float>(a.H), mean = tot.h / h;
+  const Sum2 m = add2(Sum2{mean, (fmaf(-mean, h, tot.h) + tot.l) / h}, Sum2{a.eps, 0.f});
+  const float r0 = 1.0f / sqrtf(m.h), q0 = m.h * r0;
+  const float left = fmaf(-q0, r0, 1.0f) - (fmaf(m.h, r0, -q0) + m.l * r0) * r0;  // 1 - m r0^2
+  const float corr = left == left && r0 < INFINITY ? 0.5f * r0 * left : 0.f;
+  const float inv = r0 + corr, inv_lo = r0 < INFINITY ? (r0 - inv) + corr : 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int p = tid + j * nth;
@@ -168,6 +200,28 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 512) add_rmsnorm_kernel(const N
 #pragma unroll
       for (int i = 0; i < 8; ++i) n[i] *= g[i];
     }
+    float amax = 0.f;
+    if (a.q) {  // H % 32 == 0: a block's four lanes are all there or none
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(n[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // A scale that is twice as large for a last bit of n: decide by the exact
+      // product.  About one block in a million; without it, every fourth call at
+      // 16373 x 7168 has one of its 3.7 million scales twice the definition's.
+      if (near_power(amax)) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = a.gain && ok ? load_elem(a.gain, a.gain_fmt, 8 * p + i) : 1.0f;
+          n[i] = norm_odd(y[j][i], inv, inv_lo, g);
+          amax = fmaxf(amax, fabsf(n[i]));
+        }
+        const unsigned quad = 0xfu << (lane & 28);
+        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+      }
+    }
     if (a.out && ok) {
       if (WIDE) {
         store8(a.out, a.out_fmt, t * a.H + 8 * p, n);
@@ -177,16 +231,11 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 512) add_rmsnorm_kernel(const N
           if (8 * p + i < a.H) store_elem(a.out, a.out_fmt, t * a.H + 8 * p + i, n[i]);
       }
     }
-    if (a.q) {  // H % 32 == 0: a block's four lanes are all there or none
+    if (a.q) {
       const uint4 b = make_uint4(pack_bf16(n[0], n[1]), pack_bf16(n[2], n[3]), pack_bf16(n[4], n[5]), pack_bf16(n[6], n[7]));
       float f[8];
       unpack8(b, f);
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int X = mx_scale_exp(amax);
+      const int X = mx_scale_exp(bf16_bits_to_f32(pack_bf16(amax, 0.f) & 0xffffu));  // rounding keeps the order
       const float s = exp2i(-X);
       uint32_t c[4];
 #pragma unroll
@@ -225,9 +274,9 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
                     wide_rows(a.sum, a.res_fmt, a.lds, a.T) && wide_rows(a.out, a.out_fmt, a.H, a.T) &&
                     wide_rows(a.gain, a.gain_fmt, 0, 1);
   // four pieces a thread keep 224 threads x 4 rows of 7168 in flight per SM
-  // (152 us against 177 us with two, 16373 rows); shorter rows need the
-  // threads more (2.3 against 2.8 us for 8 rows of 4096)
-  return a.H <= 4096 ? launch<2>(a, wide, s) : launch<4>(a, wide, s);
+  // (two pieces: 16% slower at 16373 rows); shorter rows need the threads more
+  // (2.3 against 2.8 us for 8 rows of 4096)
+  return a.H <= 4096 ? launch<2>(a, wide, s) : (a.H <= 14336 ? launch<4>(a, wide, s) : launch<5>(a, wide, s));
 }
 
 }  // namespace moe
