@@ -697,7 +697,8 @@ int moe_add_rmsnorm(const void* x, int x_fmt, int64_t ldx, const void* res, int 
 int moe_route_scored(const float* logits, int64_t ldl, const float* bias, int T, int E, int k, int score, int n_group,
                      int topk_group, int group_top, int renorm, float scale, int32_t* ids, float* w, uint32_t* dev_err,
                      void* stream) {
-  if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E) return fail(MOE_ERR_ARG, "moe_route_scored: bad shape");
+  if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E || static_cast<int64_t>(T) * k >= (1LL << 31))
+    return fail(MOE_ERR_ARG, "moe_route_scored: bad shape");
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_ARG, "moe_route_scored: score");
   if (n_group < 1 || n_group > 32 || E % n_group || topk_group < 1 || topk_group > n_group)
     return fail(MOE_ERR_ARG, "moe_route_scored: groups (n_group <= 32 dividing E, 1 <= topk_group <= n_group)");
@@ -730,7 +731,8 @@ int moe_gather_mxfp8(const uint8_t* x_q, const uint8_t* x_scale, const int32_t* 
 int moe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const float* bias, int act, const void* res,
                int res_fmt, int64_t ldr, int T, int N, int K, void* out, int out_fmt, int64_t ldo, uint32_t* dev_err,
                void* stream) {
-  if (T < 0 || N < 1 || K < 1 || N > (1 << 29)) return fail(MOE_ERR_ARG, "moe_linear: bad shape");
+  if (T < 0 || N < 1 || K < 1 || T > (1 << 30) || N > (1 << 29) || K > (1 << 30))
+    return fail(MOE_ERR_ARG, "moe_linear: bad shape (T, K <= 2^30, N <= 2^29)");
   if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return fail(MOE_ERR_ARG, "moe_linear: act");
   if (!row_fmt(out_fmt) || (res && !row_fmt(res_fmt))) return fail(MOE_ERR_ARG, "moe_linear: formats are BF16 or F32");
   if (T == 0) return MOE_OK;

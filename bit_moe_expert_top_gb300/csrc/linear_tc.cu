@@ -691,13 +691,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
         if (P.split > 1) {
           // to the owner of the columns: [part][column pair][128 rows] x 2 floats
           const int own = nt / P.split;
+          const uint32_t dst = smem_u32(stages + P.recv_off) + (kpart * (own / 2) * 128 + q * 32 + lane) * 8;
+          int to = c0 / own, pair = (c0 - to * own) / 2;
 #pragma unroll
           for (int c = 0; c < CW; c += 2) {
-            const int to = (c0 + c) / own, pair = (c0 + c - to * own) / 2;
-            const uint32_t dst = smem_u32(stages + P.recv_off) +
-                                 ((kpart * (own / 2) + pair) * 128 + q * 32 + lane) * 8;
             const uint32_t peer = to * CG + side;
-            st_async_f32x2(map_rank(dst, peer), v[c], v[c + 1], map_rank(smem_u32(recv), peer));
+            st_async_f32x2(map_rank(dst + pair * 1024, peer), v[c], v[c + 1], map_rank(smem_u32(recv), peer));
+            if (2 * ++pair == own) {
+              pair = 0;
+              ++to;
+            }
           }
         } else if (P.vec_io) {
           auto next = [&] { fetch_res(i + 1); };
@@ -917,7 +920,7 @@ Plan choose(const LinearArgs& a) {
     const int most = cg == 1 ? 128 : (sum ? 224 : 256);
     const int64_t mb = (rows + 128 * cg - 1) / (128 * cg);
     for (int split = 1; cg * split <= 8; split *= 2) {
-      if (split > 1 && (kb < 2 * split || mb > 152)) break;
+      if (split > 1 && (kb < 2 * split || mb > matmul_ctas())) break;
       const int64_t slots = cluster_slots(cg * split);
       if (slots < 1) continue;
       const float stages = static_cast<float>((kb + split - 1) / split);

@@ -258,7 +258,7 @@ template <int V>
 cudaError_t launch(const NormArgs& a, bool wide, cudaStream_t s) {
   const int threads = (((a.H + 7) / 8 + V - 1) / V + 31) / 32 * 32;
   const int rows = threads == 32 ? 8 : 1;
-  const dim3 grid((a.T + rows - 1) / rows), block(threads, rows);
+  const dim3 grid((a.T - 1) / rows + 1), block(threads, rows);
   if (!wide) return launch_pdl(add_rmsnorm_kernel<V, false, false, 0>, grid, block, 0, s, a);
   return a.x_fmt == MOE_FMT_F32 ? launch_wide<V, true>(a, grid, block, s) : launch_wide<V, false>(a, grid, block, s);
 }

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NPL <= 12 ? 12 : (NPL <= 16 
 }  // namespace
 
 cudaError_t launch_route_scored(const RouteArgs& a, cudaStream_t s) {
-  const dim3 grid((a.T + kRouteWarps - 1) / kRouteWarps), block(kRouteWarps * 32);
+  const dim3 grid((a.T - 1) / kRouteWarps + 1), block(kRouteWarps * 32);
   const size_t smem = a.n_group > 1 ? static_cast<size_t>(kRouteWarps) * a.E * sizeof(float) : 0;
   if (a.E <= 128) return launch_pdl(route_scored_kernel<4>, grid, block, smem, s, a);
   if (a.E <= 256) return launch_pdl(route_scored_kernel<8>, grid, block, smem, s, a);
