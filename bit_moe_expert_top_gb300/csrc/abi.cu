@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "block_ops.cuh"
 #include "internal.cuh"
 #include "layer_args.cuh"
 

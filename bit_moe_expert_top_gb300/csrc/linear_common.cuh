@@ -2,8 +2,8 @@
 #pragma once
 #include <stdint.h>
 
+#include "block_ops.cuh"
 #include "common.cuh"
-#include "internal.cuh"
 
 namespace moe {
 

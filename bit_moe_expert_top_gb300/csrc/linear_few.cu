@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "block_ops.cuh"
 #include "common.cuh"
 #include "internal.cuh"
 #include "linear_common.cuh"

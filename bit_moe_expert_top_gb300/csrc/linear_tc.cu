@@ -44,6 +44,7 @@
 
 #include <atomic>
 
+#include "block_ops.cuh"
 #include "common.cuh"
 #include "internal.cuh"
 #include "linear_common.cuh"

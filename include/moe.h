@@ -582,7 +582,7 @@ MOE_API int moe_gather_mxfp8(const uint8_t* x_q, const uint8_t* x_scale, const i
  * x bf16 [T][K], W bf16 [N][K] (MOE_ACT_SWIGLU: [2N][K], gate rows first, and
  * bias 2N), bias float nullable, res BF16 / F32 nullable, out BF16 / F32; rows
  * of x, W, res, out ldx, ldw, ldr, ldo apart.  res may be out itself (same
- * format and stride).  T >= 0, N, K >= 1, any of them odd; pointers aligned to
+ * format and stride).  0 <= T <= 2^30, 1 <= K <= 2^30, 1 <= N <= 2^29, any of them odd; pointers aligned to
  * their elements.  The tensor cores take x and W whose base and row stride are multiples of 16
  * bytes, with K a multiple of 8 (SWIGLU: N a multiple of 16); others run on a
  * slower CUDA-core kernel.  Sums of the fp32 output are kept in fp32 over at
