@@ -91,12 +91,47 @@ MOE_D float norm_odd(float y, float ih, float il, float g) {
 // where its bf16 rounding becomes the next power of two.
 MOE_D bool near_power(float amax) { return (__float_as_uint(amax) & 0x7fffffu) - 0x7f7ff8u <= 16u; }
 
+// y = x + res of one row into shared memory (and sum), 32 consecutive elements
+// per warp access, eight rounds' loads in flight.
+template <typename X>
+MOE_D void stage_row(const NormArgs& a, int64_t t, int tid, int nth, float* buf) {
+  constexpr int B = 8;
+  const X* x = static_cast<const X*>(a.x) + t * a.ldx;
+  for (int i0 = tid; i0 < a.H; i0 += B * nth) {
+    X v[B];
+    float r[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (i0 + b * nth < a.H) v[b] = x[i0 + b * nth];
+    if (a.res) {
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (i0 + b * nth < a.H) r[b] = load_elem(a.res, a.res_fmt, t * a.ldr + i0 + b * nth);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = i0 + b * nth;
+      if (i >= a.H) break;
+      float y;
+      if constexpr (sizeof(X) == 4)
+        y = v[b];
+      else
+        y = bf16_bits_to_f32(v[b]);
+      if (a.res) y += r[b];
+      if (a.sum) store_elem(a.sum, a.res_fmt, t * a.lds + i, y);
+      buf[i] = y;
+    }
+  }
+}
+
 // One CTA per row (rows of one warp: eight a CTA), the whole row in registers:
 // thread i of the row holds the 8-element pieces i, i + threads, ... (V of
 // them), so x and res are read once: bound by DRAM, 155 us at 16373 x 7168 with
 // bf16 residual and MXFP8 output (6850 GB/s, 1.01 of the copy rate).  Four
 // lanes hold one MXFP8 block.  WIDE: 16-byte accesses, formats X32 / RES (0
-// none, 1 bf16, 2 fp32); else element by element, formats read from the
+// none, 1 bf16, 2 fp32); else the row passes through shared memory, so that a
+// warp's accesses are 32 consecutive elements (8 lanes' elements apart they
+// took 132 us for 7561 rows of 3287 instead of 93), formats read from the
 // arguments.  Both sum in the same order, and V depends on H alone: a row's
 // bits depend neither on alignment nor on T.
 template <int V, bool WIDE, bool X32, int RES>
@@ -109,6 +144,14 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
   const int tid = threadIdx.x, lane = tid & 31, nth = blockDim.x;
   const int n8 = (a.H + 7) / 8;
   const bool has_res = WIDE ? RES != 0 : a.res != nullptr;
+  extern __shared__ float row_mem[];
+  float* buf = row_mem + threadIdx.y * (n8 * 8);  // !WIDE: the row's y, then n
+  auto row_sync = [&] {
+    if (nth > 32)
+      __syncthreads();
+    else
+      __syncwarp();
+  };
   Raw8<X32> rx[V];
   Raw8<RES == 2> rr[V];
   if (WIDE) {
@@ -119,6 +162,14 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       rx[j].load(a.x, t * a.ldx + 8 * p);
       if (RES) rr[j].load(a.res, t * a.ldr + 8 * p);
     }
+  }
+  if (!WIDE) {
+    if (a.x_fmt == MOE_FMT_F32)
+      stage_row<float>(a, t, tid, nth, buf);
+    else
+      stage_row<uint16_t>(a, t, tid, nth, buf);
+    for (int i = a.H + tid; i < n8 * 8; i += nth) buf[i] = 0.f;
+    row_sync();
   }
   float y[V][8];
   float ss = 0.f;
@@ -140,21 +191,9 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 8 * p + i;
-        y[j][i] = e < a.H ? load_elem(a.x, a.x_fmt, t * a.ldx + e) : 0.f;
-        if (has_res && e < a.H) y[j][i] += load_elem(a.res, a.res_fmt, t * a.ldr + e);
-      }
+      for (int i = 0; i < 8; ++i) y[j][i] = buf[8 * p + i];
     }
-    if (has_res && a.sum) {
-      if (WIDE) {
-        store8(a.sum, a.res_fmt, t * a.lds + 8 * p, y[j]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (8 * p + i < a.H) store_elem(a.sum, a.res_fmt, t * a.lds + 8 * p + i, y[j][i]);
-      }
-    }
+    if (WIDE && has_res && a.sum) store8(a.sum, a.res_fmt, t * a.lds + 8 * p, y[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
   }
@@ -228,8 +267,7 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
         store8(a.out, a.out_fmt, t * a.H + 8 * p, n);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (8 * p + i < a.H) store_elem(a.out, a.out_fmt, t * a.H + 8 * p + i, n[i]);
+        for (int i = 0; i < 8; ++i) buf[8 * p + i] = n[i];
       }
     }
     if (a.q) {
@@ -247,6 +285,10 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       }
     }
   }
+  if (!WIDE && a.out) {
+    row_sync();
+    for (int i = tid; i < a.H; i += nth) store_elem(a.out, a.out_fmt, t * a.H + i, buf[i]);
+  }
 }
 
 template <int V, bool X32>
@@ -260,7 +302,12 @@ cudaError_t launch(const NormArgs& a, bool wide, cudaStream_t s) {
   const int threads = (((a.H + 7) / 8 + V - 1) / V + 31) / 32 * 32;
   const int rows = threads == 32 ? 8 : 1;
   const dim3 grid((a.T - 1) / rows + 1), block(threads, rows);
-  if (!wide) return launch_pdl(add_rmsnorm_kernel<V, false, false, 0>, grid, block, 0, s, a);
+  if (!wide) {
+    const int smem = rows * ((a.H + 7) / 8 * 8) * static_cast<int>(sizeof(float));
+    cudaError_t e = set_smem_limit(add_rmsnorm_kernel<V, false, false, 0>, 16384 * sizeof(float));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(add_rmsnorm_kernel<V, false, false, 0>, grid, block, smem, s, a);
+  }
   return a.x_fmt == MOE_FMT_F32 ? launch_wide<V, true>(a, grid, block, s) : launch_wide<V, false>(a, grid, block, s);
 }
 
