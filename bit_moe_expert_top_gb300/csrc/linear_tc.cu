@@ -60,8 +60,7 @@ constexpr int kATile = 128 * kBK * 2;
 constexpr int kChunk = 8;          // stages per accumulation of an fp32 output (512 of K)
 constexpr int kCtl = 1024;         // barriers and flags
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 232448;   // one CTA per SM
-constexpr int kSmemHalf = 115712;  // two
+constexpr int kSmemMax = 232448;
 
 struct TcParams {
   LinearArgs a;
@@ -90,11 +89,12 @@ MOE_D uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// Two floats to a CTA of the cluster, counted by that CTA's mbarrier.
-MOE_D void st_async_f32x2(uint32_t addr, float x, float y, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
-               "f"(x), "f"(y), "r"(bar)
-               : "memory");
+// Four floats to a CTA of the cluster, counted by that CTA's mbarrier.
+MOE_D void st_async_f32x4(uint32_t addr, float x, float y, float z, float w, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+      "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar)
+      : "memory");
 }
 MOE_D void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
@@ -440,9 +440,15 @@ MOE_D void emit_tile(const LinearArgs& a, const Bias& bias, const float (&v)[CW]
 }
 
 // NT: most tokens a tile of this instance has (nt <= NT); SUM: fp32 outputs
-// (K accumulated in several chunks, NT / 2 registers of sums), else bf16.
-template <int CG, int NT, bool SUM>
-__global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
+// (K accumulated in several chunks, NT / 2 registers of sums), else bf16;
+// SPLIT: whether K is split over the CTAs (pairs) of a cluster.  Single CTAs
+// have an instance for each (the epilogue is bound by fetching instructions
+// and short of registers: 32 x 384 x 4096 5.7 us against 6.4 in one instance);
+// pairs decide at run time (an unsplit instance of their own was slower, 165
+// against 156 us at 8192 tokens SwiGLU).
+enum { kNever = 0, kAlways = 1, kEither = 2 };
+template <int CG, int NT, bool SUM, int SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                                 const __grid_constant__ CUtensorMap tm_x,
                                                                 const __grid_constant__ TcParams P) {
   constexpr int CW = (CG == 2 && !SUM) ? 32 : 16;  // columns per epilogue step
@@ -461,14 +467,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool glu = a.act == MOE_ACT_SWIGLU;
   const int ST = P.stages, kStage = P.stage_bytes, nt = P.nt;
-  const int csize = CG * P.split;
+  const bool split = SPLIT == kEither ? P.split > 1 : SPLIT == kAlways;
+  const int csize = split ? CG * P.split : CG;
   const uint32_t rank = csize > 1 ? cluster_rank() : 0;
   const int side = CG == 2 ? static_cast<int>(rank & 1) : 0;  // CTA of the pair
-  const int kpart = static_cast<int>(rank) / CG;
+  const int kpart = split ? static_cast<int>(rank) / CG : 0;
   const bool lead = side == 0;
   const int unit = blockIdx.x / csize, units = gridDim.x / csize;  // the cluster walks tiles unit, unit + units, ...
-  const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * kpart / P.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (kpart + 1) / P.split);
+  const int kb0 = split ? static_cast<int>(static_cast<int64_t>(P.kblocks) * kpart / P.split) : 0;
+  const int kb1 = split ? static_cast<int>(static_cast<int64_t>(P.kblocks) * (kpart + 1) / P.split) : P.kblocks;
   const int nchunk = (kb1 - kb0 + P.chunk - 1) / P.chunk;
 
   if (tid == 0) {
@@ -484,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
     }
     mbar_init(recv, 1);
     fence_barrier_init();
-    if (P.split > 1) mbar_arrive_expect_tx(recv, nt * 512);
+    if (split) mbar_arrive_expect_tx(recv, nt * 512);
   }
   if (warp == 1) {
     tm_alloc_cg<CG>(tmem_s, P.cols);
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
   };
   // split with the ring as receive buffer: every CTA's MMAs are done before a part is sent
   auto ring_free = [&]() {
-    if (P.split > 1 && !P.recv_own) {
+    if (split && !P.recv_own) {
       cluster_arrive();
       cluster_wait();
     }
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
     const int cb = warp < 6 ? 0 : mid, ce = warp < 6 ? mid : nt;
     const int steps = (ce - cb) / CW;
     uint8_t* own_tile = stages + P.stg_off + (warp - 2) * P.stg;
-    const bool vec_res = P.vec_io && a.res != nullptr;
+    const bool vec_res = !split && P.vec_io && a.res != nullptr;
     int ai = 0;
     bool ok = true;
     for (int tile = unit; ok && tile < P.tiles; tile += units) {
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
       if (!ok) break;
       if (SUM) fetch_res(0);
       const Bias bias = load_bias(a, n, nok);
-      const int todo = P.split == 1 ? live : steps;
+      const int todo = split ? steps : live;
 #pragma unroll 1
       for (int i = 0; i < todo; ++i) {
         const int c0 = cb + i * CW;
@@ -689,19 +696,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
         tm_ld_wait();
 #pragma unroll
         for (int c = 0; c < CW; ++c) v[c] = __uint_as_float(r[c]);
-        if (P.split > 1) {
-          // to the owner of the columns: [part][column pair][128 rows] x 2 floats
+        if (split) {
+          // to the owner of the columns: [part][4 columns][128 rows] x 4 floats
           const int own = nt / P.split;
-          const uint32_t dst = smem_u32(stages + P.recv_off) + (kpart * (own / 2) * 128 + q * 32 + lane) * 8;
-          int to = c0 / own, pair = (c0 - to * own) / 2;
+          const uint32_t dst = smem_u32(stages + P.recv_off) + (kpart * (own / 4) * 128 + q * 32 + lane) * 16;
 #pragma unroll
-          for (int c = 0; c < CW; c += 2) {
+          for (int c = 0; c < CW; c += 4) {
+            const int to = (c0 + c) / own, quad = (c0 + c - to * own) / 4;
             const uint32_t peer = to * CG + side;
-            st_async_f32x2(map_rank(dst + pair * 1024, peer), v[c], v[c + 1], map_rank(smem_u32(recv), peer));
-            if (2 * ++pair == own) {
-              pair = 0;
-              ++to;
-            }
+            st_async_f32x4(map_rank(dst + quad * 2048, peer), v[c], v[c + 1], v[c + 2], v[c + 3],
+                           map_rank(smem_u32(recv), peer));
           }
         } else if (P.vec_io) {
           auto next = [&] { fetch_res(i + 1); };
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
   tm_fence_before();
   if (csize > 1) cluster_arrive();
 
-  if (P.split > 1 && warp >= 2) {  // one tile per cluster: add the parts of this CTA's share of the columns
+  if (split && warp >= 2) {  // one tile per cluster: add the parts of this CTA's share of the columns
     int mb, tb;
     tile_of(unit, mb, tb);
     const int q = warp & 3;
@@ -730,35 +734,59 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) linear_tc_kernel(c
     const int64_t n = glu ? static_cast<int64_t>(rb) * 64 + q * 16 + (lane & 15)
                           : static_cast<int64_t>(rb) * 128 + q * 32 + lane;
     const bool nok = n < a.N;
-    const int own = nt / P.split, pairs = own / 2;
+    const int own = nt / P.split, quads = own / 4;
     const int64_t t0 = static_cast<int64_t>(tb) * nt + kpart * own;
-    const float2* got = reinterpret_cast<const float2*>(stages + P.recv_off) + q * 32 + lane;
+    const float4* got = reinterpret_cast<const float4*>(stages + P.recv_off) + q * 32 + lane;
     const bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(recv, 0, a.wait));
     if (!ok && lane == 0) set_err(a.dev_err, MOE_DEVERR_TIMEOUT);
-    auto add = [&](int p, float& x, float& y) {
-      float2 s = got[p * 128];
-      for (int r = 1; r < P.split; ++r) {
-        const float2 g = got[(r * pairs + p) * 128];
-        s.x += g.x;
-        s.y += g.y;
-      }
-      x = s.x;
-      y = s.y;
-    };
-    const int h = warp < 6 ? 0 : 1;
-    int p = h * 4;
-    for (; ok && p + 4 <= pairs; p += 8) {
-      float v[8];
+    // columns 4 s .. + 3 of the share, over the parts in order
+    auto add = [&](int s, float* v) {
+      float4 x = got[s * 128];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) add(p + u, v[2 * u], v[2 * u + 1]);
-      const int64_t t = t0 + 2 * p, left = a.T - t;
-      if (left > 0) emit<8>(a, v, t, left < 8 ? static_cast<int>(left) : 8, n, nok, lane);
+      for (int r = 1; r < 8; ++r) {
+        if (r >= P.split) break;
+        const float4 g = got[(r * quads + s) * 128];
+        x.x += g.x;
+        x.y += g.y;
+        x.z += g.z;
+        x.w += g.w;
+      }
+      v[0] = x.x;
+      v[1] = x.y;
+      v[2] = x.z;
+      v[3] = x.w;
+    };
+    const int h = warp < 6 ? 0 : 1;  // the quarter's two warps take turns
+    int done = 0;                    // quads finished through shared tiles
+    if (P.vec_io) {
+      uint8_t* own_tile = stages + P.stg_off + (warp - 2) * P.stg;
+      const int n0 = glu ? rb * 64 + q * 16 : rb * 128 + q * 32;
+      const Bias bias = load_bias(a, n, nok);
+      done = quads / (CW / 4) * (CW / 4);
+      for (int s = h * (CW / 4); ok && s < done; s += CW / 2) {
+        const int64_t t = t0 + 4 * s;
+        if (t >= a.T || n0 >= a.N) break;  // warp-uniform
+        uint4 rr[CW / 4] = {};
+        if (a.res) {
+          if (a.res_fmt == MOE_FMT_F32)
+            glu ? load_res<float, CW, 16>(a, rr, t, n0, lane) : load_res<float, CW, 32>(a, rr, t, n0, lane);
+          else
+            glu ? load_res<uint16_t, CW, 16>(a, rr, t, n0, lane) : load_res<uint16_t, CW, 32>(a, rr, t, n0, lane);
+        }
+        float v[CW];
+#pragma unroll
+        for (int u = 0; u < CW / 4; ++u) add(s + u, v + 4 * u);
+        if (glu)
+          emit_tile<CW, SUM, true>(a, bias, v, rr, [] {}, own_tile, t, n0, lane);
+        else
+          emit_tile<CW, SUM, false>(a, bias, v, rr, [] {}, own_tile, t, n0, lane);
+      }
     }
-    for (p = pairs / 4 * 4 + h; ok && p < pairs; p += 2) {
-      float v[2];
-      add(p, v[0], v[1]);
-      const int64_t t = t0 + 2 * p, left = a.T - t;
-      if (left > 0) emit<2>(a, v, t, left < 2 ? static_cast<int>(left) : 2, n, nok, lane);
+    for (int s = done + h; ok && s < quads; s += 2) {
+      float v[4];
+      add(s, v);
+      const int64_t t = t0 + 4 * s, left = a.T - t;
+      if (left > 0) emit<4>(a, v, t, left < 4 ? static_cast<int>(left) : 4, n, nok, lane);
     }
   }
   __syncthreads();
@@ -788,8 +816,12 @@ bool io_rows(const void* p, int fmt, int64_t ld, int T) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (T <= 1 || ld * sz % 16 == 0);
 }
 
-template <int CG, int NT, bool SUM>
-cudaError_t launch(const LinearArgs& a, int nt, int split, cudaStream_t s) {
+struct Plan {
+  int cg, nt, split;
+};
+
+template <int CG, int NT, bool SUM, int SPLIT>
+cudaError_t launch_plan(const LinearArgs& a, int nt, int split, cudaStream_t s) {
   const bool glu = a.act == MOE_ACT_SWIGLU;
   CUtensorMap tw, tx;
   const cuuint64_t ldw = static_cast<cuuint64_t>(a.N > 1 || glu ? a.ldw : a.K) * 2;
@@ -826,21 +858,17 @@ cudaError_t launch(const LinearArgs& a, int nt, int split, cudaStream_t s) {
   P.stage_bytes = kATile + nt / CG * kBK * 2;
   P.cols = 32;
   while (P.cols < static_cast<uint32_t>(2 * nt)) P.cols *= 2;
-  P.vec_io = split == 1 && io_rows(a.out, a.out_fmt, a.ldo, a.T) && (!a.res || io_rows(a.res, a.res_fmt, a.ldr, a.T));
+  P.vec_io = io_rows(a.out, a.out_fmt, a.ldo, a.T) && (!a.res || io_rows(a.res, a.res_fmt, a.ldr, a.T));
   constexpr int CW = (CG == 2 && !SUM) ? 32 : 16;
   const int widest = a.out_fmt == MOE_FMT_F32 || (a.res && a.res_fmt == MOE_FMT_F32) ? 4 : 2;
   P.stg = P.vec_io ? CW * (glu ? 16 : 32) * widest : 0;
   const int staging = 8 * P.stg;
   P.recv_own = split > 1 && nt * 512 <= 32768;
-  const int behind = P.recv_own ? nt * 512 : staging;
-  // a decode-sized call is small enough for two CTAs per SM, so that the next
-  // call's set-up overlaps this one's end; five stages of 18 KB on every SM
-  // still cover the DRAM latency
-  const int most_smem = NT <= 32 ? kSmemHalf : kSmemMax;
-  P.stages = (most_smem - kCtl - 1024 - behind) / P.stage_bytes;
+  const int behind = staging + (P.recv_own ? nt * 512 : 0);
+  P.stages = (kSmemMax - kCtl - 1024 - behind) / P.stage_bytes;
   if (P.stages > kMaxStages) P.stages = kMaxStages;
   P.stg_off = P.stages * P.stage_bytes;
-  P.recv_off = P.recv_own ? P.stg_off : 0;
+  P.recv_off = P.recv_own ? P.stg_off + staging : 0;
   if (split > 1 && !P.recv_own && nt * 512 > P.stages * P.stage_bytes) return cudaErrorInvalidValue;
 
   const int csize = CG * split;
@@ -850,7 +878,7 @@ cudaError_t launch(const LinearArgs& a, int nt, int split, cudaStream_t s) {
     units = units < most ? units : most;
   }
   const int smem = kCtl + 1024 + P.stages * P.stage_bytes + behind;
-  e = set_smem_limit(linear_tc_kernel<CG, NT, SUM>, kSmemMax);
+  e = set_smem_limit(linear_tc_kernel<CG, NT, SUM, SPLIT>, kSmemMax);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * csize);
@@ -865,12 +893,17 @@ cudaError_t launch(const LinearArgs& a, int nt, int split, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = csize > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, NT, SUM>, tw, tx, P);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<CG, NT, SUM, SPLIT>, tw, tx, P);
 }
 
-struct Plan {
-  int cg, nt, split;
-};
+template <int CG, int NT, bool SUM>
+cudaError_t launch(const LinearArgs& a, const Plan& p, cudaStream_t s) {
+  if constexpr (CG == 2)
+    return launch_plan<CG, NT, SUM, kEither>(a, p.nt, p.split, s);
+  else
+    return p.split > 1 ? launch_plan<CG, NT, SUM, kAlways>(a, p.nt, p.split, s)
+                       : launch_plan<CG, NT, SUM, kNever>(a, p.nt, 1, s);
+}
 
 // Clusters of `csize` CTAs that the device holds at once, one CTA per SM (SMs
 // of a partly used GPC are lost to large clusters: 36 of 4 and 15 of 8 on 152
@@ -890,8 +923,8 @@ int cluster_slots(int csize) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (set_smem_limit(linear_tc_kernel<1, 128, false>, kSmemMax) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, linear_tc_kernel<1, 128, false>, &cfg) != cudaSuccess || n <= 0) {
+    if (set_smem_limit(linear_tc_kernel<1, 128, false, kNever>, kSmemMax) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, linear_tc_kernel<1, 128, false, kNever>, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       n = d.sms / csize;
     }
@@ -927,7 +960,7 @@ Plan choose(const LinearArgs& a) {
       const float stages = static_cast<float>((kb + split - 1) / split);
       for (int nt = step; nt <= most && nt < a.T + step; nt += step) {
         const int64_t tiles = mb * ((a.T + nt - 1) / nt);
-        if (split > 1 && tiles > slots) continue;
+        if (split > 1 && (tiles > slots || nt % (4 * split))) continue;  // parts move four columns at a time
         const float mma = 0.00134f * nt, tma = 0.00145f * (128 + nt / cg);
         const float main = stages * (mma > tma ? mma : tma);
         const float epi = 0.3f + 0.007f * nt * (sum ? 2 : 1);
@@ -956,9 +989,8 @@ bool linear_tc_supported(const LinearArgs& a) {
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s) {
   const Plan p = choose(a);
   const bool sum = a.out_fmt == MOE_FMT_F32;
-  if (p.nt <= 32 && p.cg == 1) return sum ? launch<1, 32, true>(a, p.nt, p.split, s) : launch<1, 32, false>(a, p.nt, p.split, s);
-  if (p.cg == 1) return sum ? launch<1, 128, true>(a, p.nt, p.split, s) : launch<1, 128, false>(a, p.nt, p.split, s);
-  return sum ? launch<2, 224, true>(a, p.nt, p.split, s) : launch<2, 256, false>(a, p.nt, p.split, s);
+  if (p.cg == 1) return sum ? launch<1, 128, true>(a, p, s) : launch<1, 128, false>(a, p, s);
+  return sum ? launch<2, 224, true>(a, p, s) : launch<2, 256, false>(a, p, s);
 }
 
 }  // namespace moe
