@@ -83,6 +83,8 @@ MOE_D uint32_t cluster_rank() {
   return r;
 }
 MOE_D void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+// Orders no memory: for barriers that only keep a CTA alive.
+MOE_D void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 MOE_D void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 MOE_D uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -96,8 +98,11 @@ MOE_D void st_async_f32x4(uint32_t addr, float x, float y, float z, float w, uin
       "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar)
       : "memory");
 }
+// Arrival on a barrier of the pair's other CTA.  It orders TMEM reads, which
+// the tcgen05 fences do; a release at cluster scope would also wait for the
+// warp's global stores (the membar stall was the epilogue's largest).
 MOE_D void mbar_arrive_remote(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // As mbar_wait, with the acquire at cluster scope (arrivals of the peer CTA).
 MOE_D bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, long long limit) {
@@ -569,8 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
       for (int tile = unit; ok && tile < P.tiles; tile += units) {
         for (int kc = kb0; ok && kc < kb1; kc += P.chunk, ++ai) {
           const int b = ai & 1;
-          ok = CG == 2 ? mbar_wait_cluster(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait)
-                       : mbar_wait(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait);
+          ok = mbar_wait(&acc_empty[b], ((ai >> 1) & 1) ^ 1, a.wait);
           if (!ok) break;
           tm_fence_after();
           const uint32_t d = tmem + b * nt;
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
   }
   __syncwarp();
   tm_fence_before();
-  if (csize > 1) cluster_arrive();
+  if (csize > 1) cluster_arrive_relaxed();
 
   if (split && warp >= 2) {  // one tile per cluster: add the parts of this CTA's share of the columns
     int mb, tb;
@@ -940,8 +944,8 @@ int cluster_slots(int csize) {
 // their epilogues but the last; nothing is faster than the weights come from
 // DRAM; a split adds the exchange of partial sums, a pair its set-up.  The
 // constants are a least-squares fit to 660 timed (shape, tile, split)
-// combinations of 35 shapes: the choice is the fastest for 29 of them, 13%
-// off at worst (T 512, N 4096, K 4096: 23.7 against 20.9 us), 0.9% on average.
+// combinations of 35 shapes: the choice is the fastest or within 1% of it for
+// 33 of them, 5% off at worst (T 200, N 1000, K 520: 5.3 against 5.1 us).
 Plan choose(const LinearArgs& a) {
   const bool sum = a.out_fmt == MOE_FMT_F32;
   const int64_t rows = a.act == MOE_ACT_SWIGLU ? 2 * static_cast<int64_t>(a.N) : a.N;
