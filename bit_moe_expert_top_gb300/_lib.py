@@ -98,16 +98,12 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return None if t is None else t if isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:  # the handle alone: building the Stream object takes 2.9 us per call here, this 0.4
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:  # the handle alone: building the Stream object takes 2.9 us per call here, this 0.2
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -291,65 +287,65 @@ def _refuse(who: str, what: str):
     raise MoEError(MOE_ERR_ARG, f"{who}: {what}")
 
 
-def _fmt(who, t) -> int:
-    if t is None:
-        return FMT_NONE
+def _fmt(who: str, t) -> int:
     f = _FMT_OF.get(t.dtype)
     if f is None:
         _refuse(who, f"dtype {t.dtype}")
     return f
 
 
-def _rows(who, t, T: int, cols: int) -> int:
-    """Row stride of a [T, cols] tensor whose rows are contiguous (0: no tensor)."""
+def _mat(who: str, t, T: int, cols: int):
+    """(address, format, row stride) of a [T, cols] tensor whose rows are contiguous."""
     if t is None:
-        return 0
+        return None, FMT_NONE, 0
     s = t.stride()
     if t.shape != (T, cols) or (s[1] != 1 and cols > 1):
         _refuse(who, f"shape {tuple(t.shape)} / strides {s}, wanted contiguous rows [{T}, {cols}]")
-    return s[0] if T > 1 else cols
+    return t.data_ptr(), _FMT_OF.get(t.dtype) or _fmt(who, t), s[0] if T > 1 else cols
 
 
-def _flat(who, t, n: int):
-    if t is not None and (t.numel() != n or not t.is_contiguous()):
+def _vec(who: str, t, n: int):
+    """Address of n contiguous elements."""
+    if t is None:
+        return None
+    if t.numel() != n or not t.is_contiguous():
         _refuse(who, f"shape {tuple(t.shape)}, wanted {n} contiguous elements")
+    return t.data_ptr()
 
 
 def moe_add_rmsnorm(x, gain, eps, res=None, sum_out=None, out=None, q=None, q_scale=None, stream=None):
     who = "moe_add_rmsnorm"
     T, H = x.shape
-    _flat(who, gain, H)
-    _flat(who, out, T * H)
-    _flat(who, q, T * H)
-    _flat(who, q_scale, T * (H // 32))
-    if sum_out is not None and (res is None or _fmt(who, sum_out) != _fmt(who, res)):
+    xp, xf, ldx = _mat(who, x, T, H)
+    rp, rf, ldr = _mat(who, res, T, H)
+    sp, sf, lds = _mat(who, sum_out, T, H)
+    if sum_out is not None and sf != rf:
         _refuse(who, "sum_out needs res, in its dtype")
-    _check(lib().moe_add_rmsnorm(_ptr(x), _fmt(who, x), _rows(who, x, T, H), _ptr(res), _fmt(who, res),
-                                 _rows(who, res, T, H), _ptr(gain), _fmt(who, gain), eps, T, H, _ptr(sum_out),
-                                 _rows(who, sum_out, T, H), _ptr(out), _fmt(who, out), _ptr(q), _ptr(q_scale),
-                                 _stream(stream)))
+    _check(lib().moe_add_rmsnorm(xp, xf, ldx, rp, rf, ldr, _vec(who, gain, H), FMT_NONE if gain is None else _fmt(who, gain),
+                                 eps, T, H, sp, lds, _vec(who, out, T * H), FMT_NONE if out is None else _fmt(who, out),
+                                 _vec(who, q, T * H), _vec(who, q_scale, T * (H // 32)), _stream(stream)))
 
 
 def moe_route_scored(logits, k, ids, w, bias=None, score=SCORE_SOFTMAX, n_group=1, topk_group=1, group_top=1,
                      renorm=True, scale=1.0, dev_err=None, stream=None):
     who = "moe_route_scored"
     T, E = logits.shape
-    _flat(who, bias, E)
-    _flat(who, ids, T * k)
-    _flat(who, w, T * k)
-    _check(lib().moe_route_scored(_ptr(logits), _rows(who, logits, T, E), _ptr(bias), T, E, k, score, n_group,
-                                  topk_group, group_top, int(bool(renorm)), scale, _ptr(ids), _ptr(w),
-                                  _ptr(dev_err), _stream(stream)))
+    lp, lf, ldl = _mat(who, logits, T, E)
+    if lf != FMT_F32 or ids.dtype is not torch.int32 or w.dtype is not torch.float32:
+        _refuse(who, "logits and w are float32, ids int32")
+    _check(lib().moe_route_scored(lp, ldl, _vec(who, bias, E), T, E, k, score, n_group, topk_group, group_top,
+                                  1 if renorm else 0, scale, _vec(who, ids, T * k), _vec(who, w, T * k), _ptr(dev_err),
+                                  _stream(stream)))
 
 
 def moe_gather_mxfp8(x_q, x_scale, inv, k, x_perm, x_perm_scale, stream=None):
     who = "moe_gather_mxfp8"
     T, H = x_q.shape
-    for t, n in ((x_q, T * H), (x_scale, T * (H // 32)), (inv, T * k), (x_perm, T * k * H),
-                 (x_perm_scale, T * k * (H // 32))):
-        _flat(who, t, n)
-    _check(lib().moe_gather_mxfp8(_ptr(x_q), _ptr(x_scale), _ptr(inv), T, k, H, _ptr(x_perm), _ptr(x_perm_scale),
-                                  _stream(stream)))
+    n, m = T * H, T * (H // 32)
+    if inv.dtype is not torch.int32:
+        _refuse(who, "inv is int32")
+    _check(lib().moe_gather_mxfp8(_vec(who, x_q, n), _vec(who, x_scale, m), _vec(who, inv, T * k), T, k, H,
+                                  _vec(who, x_perm, n * k), _vec(who, x_perm_scale, m * k), _stream(stream)))
 
 
 def moe_linear(x, w, out, bias=None, act=ACT_NONE, res=None, dev_err=None, stream=None):
@@ -357,9 +353,13 @@ def moe_linear(x, w, out, bias=None, act=ACT_NONE, res=None, dev_err=None, strea
     T, K = x.shape
     rows = w.shape[0]
     N = rows // 2 if act == ACT_SWIGLU else rows
-    if _fmt(who, x) != FMT_BF16 or _fmt(who, w) != FMT_BF16 or (act == ACT_SWIGLU and rows % 2):
+    xp, xf, ldx = _mat(who, x, T, K)
+    wp, wf, ldw = _mat(who, w, rows, K)
+    if xf != FMT_BF16 or wf != FMT_BF16 or (act == ACT_SWIGLU and rows % 2):
         _refuse(who, "x and w are bf16; SWIGLU weights have an even number of rows")
-    _flat(who, bias, rows)
-    _check(lib().moe_linear(_ptr(x), _rows(who, x, T, K), _ptr(w), _rows(who, w, rows, K), _ptr(bias), act, _ptr(res),
-                            _fmt(who, res), _rows(who, res, T, N), T, N, K, _ptr(out), _fmt(who, out),
-                            _rows(who, out, T, N), _ptr(dev_err), _stream(stream)))
+    rp, rf, ldr = _mat(who, res, T, N)
+    op, of, ldo = _mat(who, out, T, N)
+    if bias is not None and bias.dtype is not torch.float32:
+        _refuse(who, "bias is float32")
+    _check(lib().moe_linear(xp, ldx, wp, ldw, _vec(who, bias, rows), act, rp, rf, ldr, T, N, K, op, of, ldo,
+                            _ptr(dev_err), _stream(stream)))

@@ -89,3 +89,18 @@ def test_binding_refuses_tensors_it_cannot_describe(lib_path):  # noqa: F811
         L.moe_gather_mxfp8(x.view(torch.uint8)[:, :64].contiguous(), torch.zeros(4, 1, dtype=torch.uint8),
                            torch.zeros(4, 2, dtype=torch.int32), 2, torch.zeros(8, 64, dtype=torch.uint8),
                            torch.zeros(8, 2, dtype=torch.uint8), stream=0)
+
+
+def test_binding_refuses_index_and_weight_types_it_would_misread(lib_path):  # noqa: F811
+    lg, ids, w = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    for bad in ((lg.bfloat16(), ids, w), (lg, ids.long(), w), (lg, ids, w.double())):
+        with pytest.raises(L.MoEError):
+            L.moe_route_scored(bad[0], 2, bad[1], bad[2], stream=0)
+    u8 = torch.zeros(4, 64, dtype=torch.uint8)
+    with pytest.raises(L.MoEError):  # int64 positions, as randperm gives them
+        L.moe_gather_mxfp8(u8, u8[:, :2].contiguous(), torch.randperm(8), 2, torch.zeros(8, 64, dtype=torch.uint8),
+                           torch.zeros(8, 2, dtype=torch.uint8), stream=0)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(L.MoEError):
+        L.moe_linear(x, torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(4, 8),
+                     bias=torch.zeros(8, dtype=torch.bfloat16), stream=0)
