@@ -91,51 +91,94 @@ MOE_D float norm_odd(float y, float ih, float il, float g) {
 // where its bf16 rounding becomes the next power of two.
 MOE_D bool near_power(float amax) { return (__float_as_uint(amax) & 0x7fffffu) - 0x7f7ff8u <= 16u; }
 
-// y = x + res of one row into shared memory (and sum), 32 consecutive elements
-// per warp access, eight rounds' loads in flight.
-template <typename X>
-MOE_D void stage_row(const NormArgs& a, int64_t t, int tid, int nth, float* buf) {
-  constexpr int B = 8;
-  const X* x = static_cast<const X*>(a.x) + t * a.ldx;
-  for (int i0 = tid; i0 < a.H; i0 += B * nth) {
-    X v[B];
-    float r[B];
+// Rows that start `off` bytes behind a 16-byte boundary.  A load cuts 8-element
+// piece p out of the aligned 16-byte chunks it lies in; pieces with a chunk
+// that reaches over an end of the row (the first, the last, and the one before
+// a short last one) come from `edge` instead, one element per lane.  A store
+// gathers aligned chunks from the row in shared memory.  Nothing outside the
+// row is read or written.
+MOE_D int offset_of(const char* row) { return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15); }
+MOE_D char* row_of(const void* p, int fmt, int64_t elems) {
+  return static_cast<char*>(const_cast<void*>(p)) + elems * (fmt == MOE_FMT_F32 ? 4 : 2);
+}
+template <bool F32>
+struct Cut8 {
+  static constexpr int W = F32 ? 8 : 4, kElem = F32 ? 4 : 2;
+  uint32_t w[W + 4];
+  static MOE_D bool inner(int off, int p, int H) {
+    return off == 0 ? 8 * p + 8 <= H : p > 0 && (8 * p + 8) * kElem + 16 - off <= H * kElem;
+  }
+  MOE_D void load(const char* row, int off, int p) {
+    const uint4* c = reinterpret_cast<const uint4*>(row - off) + p * (W / 4);
 #pragma unroll
-    for (int b = 0; b < B; ++b)
-      if (i0 + b * nth < a.H) v[b] = x[i0 + b * nth];
-    if (a.res) {
-#pragma unroll
-      for (int b = 0; b < B; ++b)
-        if (i0 + b * nth < a.H) r[b] = load_elem(a.res, a.res_fmt, t * a.ldr + i0 + b * nth);
-    }
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int i = i0 + b * nth;
-      if (i >= a.H) break;
-      float y;
-      if constexpr (sizeof(X) == 4)
-        y = v[b];
-      else
-        y = bf16_bits_to_f32(v[b]);
-      if (a.res) y += r[b];
-      if (a.sum) store_elem(a.sum, a.res_fmt, t * a.lds + i, y);
-      buf[i] = y;
+    for (int i = 0; i <= W / 4; ++i) {
+      if (i < W / 4 || off) {
+        const uint4 v = c[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
     }
   }
+  MOE_D void get(float (&f)[8], int off) {  // the 4 W bytes that start off bytes into w
+    if (off & 8) {
+#pragma unroll
+      for (int i = 0; i < W + 2; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4) {
+#pragma unroll
+      for (int i = 0; i < W + 1; ++i) w[i] = w[i + 1];
+    }
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (off & 2));
+      unpack8(make_uint4(w[0], w[1], w[2], w[3]), f);
+    }
+  }
+};
+// Place of element i of a row in shared memory: 32 lanes that read or write
+// consecutive elements, or elements 4 or 8 apart, find them in 32 banks.  Of a
+// group of G = 4 or 8 elements, slot(G g + r) = slot(G g) ^ r.
+MOE_D int slot(int i) { return i ^ ((i >> 5) & 7); }
+// Elements [0, H) from shared memory to a row, by the row's nth threads.
+template <bool F32>
+MOE_D void put_row(char* row, int H, const float* buf, int tid, int nth) {
+  constexpr int kElem = F32 ? 4 : 2, C = 16 / kElem, fmt = F32 ? MOE_FMT_F32 : MOE_FMT_BF16;
+  const int head = min(H, ((16 - offset_of(row)) & 15) / kElem), chunks = (H - head) / C, tail = head + chunks * C;
+  for (int c = tid; c < chunks; c += nth) {
+    const int s0 = slot(C * c), s1 = slot(C * c + C);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < C; ++i) f[i] = buf[(head + i < C ? s0 : s1) ^ ((head + i) & (C - 1))];
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = F32 ? __float_as_uint(f[i]) : pack_bf16(f[2 * i], f[2 * i + 1]);
+    reinterpret_cast<uint4*>(row + head * kElem)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (tid < head) store_elem(row, fmt, tid, buf[slot(tid)]);
+  if (tail + tid < H) store_elem(row, fmt, tail + tid, buf[slot(tail + tid)]);
 }
+
+MOE_HD int row_floats(int H) { return (H + 31) / 32 * 32; }
 
 // One CTA per row (rows of one warp: eight a CTA), the whole row in registers:
 // thread i of the row holds the 8-element pieces i, i + threads, ... (V of
 // them), so x and res are read once: bound by DRAM, 155 us at 16373 x 7168 with
 // bf16 residual and MXFP8 output (6850 GB/s, 1.01 of the copy rate).  Four
-// lanes hold one MXFP8 block.  WIDE: 16-byte accesses, formats X32 / RES (0
-// none, 1 bf16, 2 fp32); else the row passes through shared memory, so that a
-// warp's accesses are 32 consecutive elements (8 lanes' elements apart they
-// took 132 us for 7561 rows of 3287 instead of 93), formats read from the
-// arguments.  Both sum in the same order, and V depends on H alone: a row's
-// bits depend neither on alignment nor on T.
+// lanes hold one MXFP8 block.  Formats X32 / RES (0 none, 1 bf16, 2 fp32).
+// WIDE: every row starts at a 16-byte boundary and H is a multiple of 8; else
+// pieces are cut out of aligned chunks, and rows of sum and out that are not at
+// a boundary pass through shared memory: bound by the issue of ~1170
+// instructions per warp and row (0.71 of the slots).  7561 rows of 3287 with
+// bf16 residual and output take 72 us (element by element through shared memory
+// 97), 3288 wide 35; 3000 x 7168 with MXFP8, x and res strided by 7173, 53 (78).
+// Both forms sum in the same order, and V depends on H alone: a row's bits
+// depend neither on alignment nor on T.  !WIDE is bound to fewer CTAs per SM
+// for its second chunks' registers (4 pieces of fp32 in 72 registers spill: 8
+// rows of 7167 7.5 us against 6.0).
 template <int V, bool WIDE, bool X32, int RES>
-__global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(V == 2 ? 256 : 448, WIDE ? (V == 2 ? 5 : 2) : (V == 2 ? 4 : (V == 4 && !X32 && RES != 2 ? 2 : 1))) add_rmsnorm_kernel(const NormArgs a) {
   __shared__ float part[32];
   pdl_wait();
   pdl_trigger();
@@ -143,34 +186,52 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
   if (t >= a.T) return;  // a whole warp: only one-warp rows share a CTA
   const int tid = threadIdx.x, lane = tid & 31, nth = blockDim.x;
   const int n8 = (a.H + 7) / 8;
-  const bool has_res = WIDE ? RES != 0 : a.res != nullptr;
-  extern __shared__ float row_mem[];
-  float* buf = row_mem + threadIdx.y * (n8 * 8);  // !WIDE: the row's y, then n
+  extern __shared__ float row_mem[];  // !WIDE: y and n of the row, whole groups of 32
+  float* buf = row_mem + threadIdx.y * row_floats(a.H);
   auto row_sync = [&] {
     if (nth > 32)
       __syncthreads();
     else
       __syncwarp();
   };
-  Raw8<X32> rx[V];
-  Raw8<RES == 2> rr[V];
-  if (WIDE) {
+  Raw8<X32> rx[WIDE ? V : 1];
+  Raw8<RES == 2> rr[WIDE ? V : 1];
+  Cut8<X32> cx[WIDE ? 1 : V];
+  Cut8<RES == 2> cr[WIDE ? 1 : V];
+  const char* xrow = row_of(a.x, X32 ? MOE_FMT_F32 : MOE_FMT_BF16, t * a.ldx);
+  const char* rrow = row_of(a.res, a.res_fmt, t * a.ldr);
+  const int xoff = offset_of(xrow), roff = offset_of(rrow);
+  auto inner = [&](int p) { return Cut8<X32>::inner(xoff, p, a.H) && (!RES || Cut8<RES == 2>::inner(roff, p, a.H)); };
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int p = tid + j * nth;
+  for (int j = 0; j < V; ++j) {
+    const int p = tid + j * nth;
+    if (WIDE) {
       if (p >= n8) continue;
       rx[j].load(a.x, t * a.ldx + 8 * p);
       if (RES) rr[j].load(a.res, t * a.ldr + 8 * p);
+    } else {
+      if (!inner(p)) continue;
+      cx[j].load(xrow, xoff, p);
+      if (RES) cr[j].load(rrow, roff, p);
     }
   }
+  __shared__ float edge_mem[WIDE ? 1 : 8][24];  // y of pieces 0, n8 - 2 and n8 - 1
+  float* edge = edge_mem[WIDE ? 0 : threadIdx.y];
   if (!WIDE) {
-    if (a.x_fmt == MOE_FMT_F32)
-      stage_row<float>(a, t, tid, nth, buf);
-    else
-      stage_row<uint16_t>(a, t, tid, nth, buf);
-    for (int i = a.H + tid; i < n8 * 8; i += nth) buf[i] = 0.f;
+    if (tid < 24) {
+      const int i = tid < 8 ? tid : 8 * (n8 - 3) + tid;
+      float v = 0.f;
+      if (i >= 0 && i < a.H) {
+        v = load_elem(xrow, X32 ? MOE_FMT_F32 : MOE_FMT_BF16, i);
+        if (RES) v += load_elem(rrow, a.res_fmt, i);
+      }
+      edge[tid] = v;
+    }
     row_sync();
   }
+  char* srow = row_of(a.sum, a.res_fmt, t * a.lds);
+  char* orow = row_of(a.out, a.out_fmt, t * a.H);
+  const bool swide = WIDE || (a.H % 8 == 0 && offset_of(srow) == 0), owide = WIDE || (a.H % 8 == 0 && offset_of(orow) == 0);
   float y[V][8];
   float ss = 0.f;
 #pragma unroll
@@ -181,21 +242,40 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       for (int i = 0; i < 8; ++i) y[j][i] = 0.f;
       continue;
     }
-    if (WIDE) {
-      rx[j].get(y[j]);
+    if (WIDE || inner(p)) {
+      if (WIDE)
+        rx[j].get(y[j]);
+      else
+        cx[j].get(y[j], xoff);
       if (RES) {
         float f[8];
-        rr[j].get(f);
+        if (WIDE)
+          rr[j].get(f);
+        else
+          cr[j].get(f, roff);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[j][i] += f[i];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[j][i] = buf[8 * p + i];
+      for (int i = 0; i < 8; ++i) y[j][i] = edge[(p == 0 ? 0 : 8 * (p - n8 + 3)) + i];
     }
-    if (WIDE && has_res && a.sum) store8(a.sum, a.res_fmt, t * a.lds + 8 * p, y[j]);
+    if (RES && a.sum) {
+      if (swide) {
+        store8(a.sum, a.res_fmt, t * a.lds + 8 * p, y[j]);
+      } else {
+        const int s = slot(8 * p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) buf[s ^ i] = y[j][i];
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(y[j][i], y[j][i], ss);
+  }
+  if (!swide && RES && a.sum) {
+    row_sync();
+    put_row<RES == 2>(srow, a.H, buf, tid, nth);
+    row_sync();
   }
   if (!a.out && !a.q) return;
   // sum over the lanes and warps, inv = ih + il = 1 / sqrt(mean + eps): the
@@ -210,6 +290,7 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
     tot = Sum2{part[0], 0.f};
     for (int w = 1; w < nth >> 5; ++w) tot = add2(tot, Sum2{part[w], 0.f});
   }
+  const bool gain16 = reinterpret_cast<uintptr_t>(a.gain) % 16 == 0;  // whatever the rows are
   const float h = static_cast<float>(a.H), mean = tot.h / h;
   const Sum2 m = add2(Sum2{mean, (fmaf(-mean, h, tot.h) + tot.l) / h}, Sum2{a.eps, 0.f});
   const float r0 = 1.0f / sqrtf(m.h), q0 = m.h * r0;
@@ -225,7 +306,7 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
     for (int i = 0; i < 8; ++i) n[i] = y[j][i] * inv;
     if (a.gain && ok) {
       float g[8];
-      if (!WIDE) {
+      if (!WIDE && (!gain16 || 8 * p + 8 > a.H)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = 8 * p + i < a.H ? load_elem(a.gain, a.gain_fmt, 8 * p + i) : 0.f;
       } else if (a.gain_fmt == MOE_FMT_F32) {
@@ -263,11 +344,12 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       }
     }
     if (a.out && ok) {
-      if (WIDE) {
+      if (owide) {
         store8(a.out, a.out_fmt, t * a.H + 8 * p, n);
       } else {
+        const int s = slot(8 * p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) buf[8 * p + i] = n[i];
+        for (int i = 0; i < 8; ++i) buf[s ^ i] = n[i];
       }
     }
     if (a.q) {
@@ -285,30 +367,39 @@ __global__ void __launch_bounds__(V == 2 ? 256 : 448, V == 2 ? 5 : 2) add_rmsnor
       }
     }
   }
-  if (!WIDE && a.out) {
+  if (!owide && a.out) {
     row_sync();
-    for (int i = tid; i < a.H; i += nth) store_elem(a.out, a.out_fmt, t * a.H + i, buf[i]);
+    if (a.out_fmt == MOE_FMT_F32)
+      put_row<true>(orow, a.H, buf, tid, nth);
+    else
+      put_row<false>(orow, a.H, buf, tid, nth);
   }
 }
 
-template <int V, bool X32>
-cudaError_t launch_wide(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
-  if (!a.res) return launch_pdl(add_rmsnorm_kernel<V, true, X32, 0>, grid, block, 0, s, a);
-  if (a.res_fmt == MOE_FMT_BF16) return launch_pdl(add_rmsnorm_kernel<V, true, X32, 1>, grid, block, 0, s, a);
-  return launch_pdl(add_rmsnorm_kernel<V, true, X32, 2>, grid, block, 0, s, a);
+template <int V, bool WIDE, bool X32, int RES>
+cudaError_t launch_one(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
+  int smem = 0;
+  if (!WIDE) {
+    smem = block.y * row_floats(a.H) * static_cast<int>(sizeof(float));
+    cudaError_t e = set_smem_limit(add_rmsnorm_kernel<V, WIDE, X32, RES>, 16384 * sizeof(float));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(add_rmsnorm_kernel<V, WIDE, X32, RES>, grid, block, smem, s, a);
+}
+template <int V, bool WIDE, bool X32>
+cudaError_t launch_res(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t s) {
+  if (!a.res) return launch_one<V, WIDE, X32, 0>(a, grid, block, s);
+  if (a.res_fmt == MOE_FMT_BF16) return launch_one<V, WIDE, X32, 1>(a, grid, block, s);
+  return launch_one<V, WIDE, X32, 2>(a, grid, block, s);
 }
 template <int V>
 cudaError_t launch(const NormArgs& a, bool wide, cudaStream_t s) {
   const int threads = (((a.H + 7) / 8 + V - 1) / V + 31) / 32 * 32;
   const int rows = threads == 32 ? 8 : 1;
   const dim3 grid((a.T - 1) / rows + 1), block(threads, rows);
-  if (!wide) {
-    const int smem = rows * ((a.H + 7) / 8 * 8) * static_cast<int>(sizeof(float));
-    cudaError_t e = set_smem_limit(add_rmsnorm_kernel<V, false, false, 0>, 16384 * sizeof(float));
-    if (e != cudaSuccess) return e;
-    return launch_pdl(add_rmsnorm_kernel<V, false, false, 0>, grid, block, smem, s, a);
-  }
-  return a.x_fmt == MOE_FMT_F32 ? launch_wide<V, true>(a, grid, block, s) : launch_wide<V, false>(a, grid, block, s);
+  if (wide)
+    return a.x_fmt == MOE_FMT_F32 ? launch_res<V, true, true>(a, grid, block, s) : launch_res<V, true, false>(a, grid, block, s);
+  return a.x_fmt == MOE_FMT_F32 ? launch_res<V, false, true>(a, grid, block, s) : launch_res<V, false, false>(a, grid, block, s);
 }
 
 bool wide_rows(const void* p, int fmt, int64_t ld, int T) {

@@ -531,8 +531,9 @@ MOE_API int moe_combine(const void* y, int y_fmt, const float* w, const int32_t*
  * be there.  sum may be res itself (in place, lds == ldr); out [T][H], q
  * [T][H], q_scale [T][H/32] are contiguous, the form the other calls read.
  * 1 <= H <= 16384; q needs H a multiple of 32, q 16-byte aligned.  Pointers
- * aligned to their elements; 16-byte aligned rows take the wide path.  NaN and infinite elements give
- * what the formula gives (their row's n is NaN or 0).  T = 0 is a no-op. */
+ * aligned to their elements; rows that start at 16-byte boundaries are faster
+ * and give the same bits.  NaN and infinite elements give what the formula
+ * gives (their row's n is NaN or 0).  T = 0 is a no-op. */
 MOE_API int moe_add_rmsnorm(const void* x, int x_fmt, int64_t ldx, const void* res, int res_fmt, int64_t ldr,
                     const void* gain, int gain_fmt, float eps, int T, int H, void* sum, int64_t lds,
                     void* out, int out_fmt, uint8_t* q, uint8_t* q_scale, void* stream);

@@ -141,6 +141,45 @@ def test_add_rmsnorm_long_rows_apart():
     assert not host(out)[0].any() and np.allclose(host(out)[1], 1.0, atol=1e-6)
 
 
+def placed(t, off):
+    """A copy of t [T, H] `off` elements behind a 16-byte boundary, rows one element further apart
+    than they are long, in a buffer of sevens; returns (buffer, view)."""
+    T, H = t.shape
+    buf = torch.full((off + T * (H + 1) + 32,), 7.0, device=DEV, dtype=t.dtype)
+    v = torch.as_strided(buf, (T, H), (H + 1, 1), off)
+    v.copy_(t)
+    return buf, v
+
+
+@pytest.mark.parametrize("H", [1, 2, 7, 8, 9, 15, 16, 17, 23, 24, 40, 261, 512, 1031, 4608])
+@pytest.mark.parametrize("xd,rd,od", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f32", "bf16", "bf16"), ("f32", "f32", "f32")])
+def test_add_rmsnorm_bits_do_not_depend_on_alignment(H, xd, rd, od):
+    """Rows at every offset from a 16-byte boundary give the bits of rows at the boundary, and
+    nothing is written beside the rows."""
+    T = 9
+    g = gen(H)
+    x, res, gn = randn(g, T, H, dtype=DT[xd]), randn(g, T, H, dtype=DT[rd], scale=5.0), 1 + randn(g, H, scale=0.2)
+    want_s = (x.float() + res.float()).to(DT[rd])
+    want = torch.empty(T, H, device=DEV, dtype=DT[od])
+    for t in range(T):  # one row a call: at the boundary whatever H is
+        row = torch.empty(1, H, device=DEV, dtype=DT[od])
+        L.moe_add_rmsnorm(x[t:t + 1].clone(), gn, 1e-5, res=res[t:t + 1].clone(), out=row)
+        want[t] = row[0]
+    for off in range(8):
+        xv, rv = placed(x, off)[1], placed(res, (3 * off + 1) % 8)[1]
+        sbuf, sv = placed(torch.zeros_like(res), (5 * off + 2) % 8)
+        obuf = torch.full((off + T * H + 32,), 7.0, device=DEV, dtype=DT[od])
+        out = torch.as_strided(obuf, (T, H), (H, 1), off)
+        gv = torch.empty(off + H, device=DEV)[off:].copy_(gn)
+        L.moe_add_rmsnorm(xv, gv, 1e-5, res=rv, sum_out=sv, out=out)
+        assert torch.equal(out, want) and torch.equal(sv, want_s), off
+        assert bool((obuf[:off] == 7).all()) and bool((obuf[off + T * H:] == 7).all())
+        sv.fill_(7)
+        assert bool((sbuf == 7).all())
+        L.moe_add_rmsnorm(xv, gv, 1e-5, res=rv, sum_out=rv, out=out)  # in place
+        assert torch.equal(out, want) and torch.equal(rv, want_s), off
+
+
 # ------------------------------------------------------------------ route
 ROUTE = [  # T, E, k, score, bias, groups, keep, best, renorm, scale
     (1, 1, 1, "softmax", False, 1, 1, 1, True, 1.0),
