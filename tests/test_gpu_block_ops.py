@@ -250,6 +250,31 @@ def test_route_scored(T, E, k, score, bias, groups, keep, best, renorm, scale):
         assert np.all(np.abs(w - want_w) <= 1e-5 * np.abs(want_w))
 
 
+@pytest.mark.parametrize("E,groups,keep", [(128, 1, 1), (129, 1, 1), (513, 1, 1), (640, 4, 2), (641, 1, 1), (768, 16, 16), (769, 1, 1),
+                                           (896, 8, 3), (897, 1, 1), (1000, 8, 8), (1024, 1, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_widths(E, groups, keep, score):
+    """Both sides of every number of experts a lane can hold; groups that all stay."""
+    test_route_scored(37, E, 8, score, True, groups, keep, 2, True, 2.5)
+
+
+def test_route_scored_all_groups_kept_is_no_groups():
+    """Masked and NaN logits among them."""
+    g = gen(11)
+    l = randn(g, 64, 256)
+    l[randn(g, 64, 256) > 1] = -float("inf")
+    l[3, 7] = float("nan")
+    l[5] = -float("inf")
+    l[6, :32] = float("nan")  # a whole group
+    b = randn(g, 256, scale=0.01)
+    r = []
+    for n in (1, 8):
+        ids, w, err = torch.empty(64, 8, device=DEV, dtype=torch.int32), torch.empty(64, 8, device=DEV), torch.zeros(1, device=DEV, dtype=torch.int32)
+        L.moe_route_scored(l, 8, ids, w, bias=b, score=L.SCORE_SIGMOID, n_group=n, topk_group=n, group_top=2, dev_err=err)
+        r.append((host(ids), host(w), int(err)))
+    assert np.array_equal(r[0][0], r[1][0]) and np.array_equal(r[0][1], r[1][1]) and r[0][2] == r[1][2]
+
+
 def test_route_scored_is_moe_route():
     """Softmax, no bias, one group, renormalised: the ids of moe_route, its weights to rounding."""
     g = gen(5)
