@@ -614,12 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_tc_kernel(const __grid_con
     // The residual of this warp's rows of a tile (split: of the columns that
     // this CTA will own) on its way to L2: the registers hold one step of it,
     // too little for DRAM's latency where a tile's MMAs are short (us: 8192 x
-    // 4096 x 256 43.6 without, 40.6; 7711 x 3648 x 144 SwiGLU, fp32 residual,
-    // 99 without, 82).  The first tile's own rows only where steps of 16-byte
-    // accesses follow (3000 x 640 x 1000 11.6 without, 10.8): the other form
-    // has all of a step's loads in flight (777 x 1900 15.9 with, 15.4 without).
+    // 4096 x 256 43.0 without, 40.2; 7711 x 3648 x 144 SwiGLU, fp32 residual,
+    // 97 without, 82).  With a longer K the MMAs hide it and the requests only
+    // cost (16384 x 7168 x 2048 301 without, 307; 1024 tokens 26.2, 26.8).  The
+    // first tile's own rows only where steps of 16-byte accesses follow (3000 x
+    // 640 x 1000 11.6 without, 10.8): the other form has all of a step's loads
+    // in flight.
+    const bool ahead = a.res != nullptr && P.kblocks <= 16;
     auto prefetch_res = [&](int tile) {
-      if (!a.res || tile >= P.tiles) return;
+      if (!ahead || tile >= P.tiles) return;
       int mb, tb;
       tile_of(tile, mb, tb);
       const int rb = mb * CG + side, n0 = glu ? rb * 64 + q * 16 : rb * 128 + q * 32;
